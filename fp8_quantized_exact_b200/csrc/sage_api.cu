@@ -9,15 +9,13 @@
 #include <mutex>
 #include <vector>
 
+#include "api_checks.cuh"
+#include "cache_common.cuh"
 #include "sage_common.cuh"
 
 using namespace sage;
 
 namespace {
-
-constexpr size_t kAlign = 1024;
-constexpr int kMaxGridYZ = 65535;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Process-wide settings; entry points may be called from several threads.
 std::atomic<int> g_mainloop{SAGE_MAINLOOP_DEFAULT};
@@ -55,34 +53,6 @@ Dims make_dims(int B, int N, int H, int D) {
   return d;
 }
 
-int check_dims(int B, int N, int H, int D) {
-  if (B < 0 || N < 0 || H < 0 || D < 0) return SAGE_ERR_INVALID_ARG;
-  if (D != 64 && D != 128) return SAGE_ERR_UNSUPPORTED;
-  // H and B are the y and z extents of the kernels' grids
-  if (B > kMaxGridYZ || H > kMaxGridYZ) return SAGE_ERR_UNSUPPORTED;
-  // keep every flat index inside int range assumptions of the kernels
-  if ((int64_t)B * H > (1 << 30) || N > (1 << 28)) return SAGE_ERR_UNSUPPORTED;
-  return SAGE_OK;
-}
-
-bool empty(int B, int N, int H) { return B == 0 || N == 0 || H == 0; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int check_view(const sage_view_bf16& v) {
-  if (!v.data) return SAGE_ERR_INVALID_ARG;
-  if (v.stride_b < 0 || v.stride_n < 0 || v.stride_h < 0) return SAGE_ERR_INVALID_ARG;
-  if (!aligned16(v.data) || (v.stride_b | v.stride_n | v.stride_h) & 7) return SAGE_ERR_UNSUPPORTED;
-  return SAGE_OK;
-}
-
-int check_out(const void* out, int64_t sb, int64_t sn, int64_t sh) {
-  if (!out) return SAGE_ERR_INVALID_ARG;
-  if (sb < 0 || sn < 0 || sh < 0) return SAGE_ERR_INVALID_ARG;
-  if (!aligned16(out) || (sb | sn | sh) & 7) return SAGE_ERR_UNSUPPORTED;
-  return SAGE_OK;
-}
-
 // Byte offsets of every region of a workspace.
 struct Layout {
   size_t status = 0;
@@ -115,18 +85,6 @@ Layout plan(int op, const Dims& d) {
   if (all3) L.sync = take(prepass_sync_bytes(d.B, d.H, d.D));  // single-launch prepasses
   L.total = off;
   return L;
-}
-
-int check_ws(void* ws, size_t bytes, size_t need) {
-  if (!ws) return SAGE_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return SAGE_ERR_WORKSPACE;
-  if (bytes < need) return SAGE_ERR_WORKSPACE;
-  return SAGE_OK;
-}
-
-template <class T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
 FusedOut fused_out(void* ws, const Layout& L, int8_t* q8, float* qs, int8_t* k8, float* ks, float* km,
@@ -166,11 +124,6 @@ int default_prepass(int B, int N, int H, int D) {
 
 int clear_status(void* ws, cudaStream_t s) {
   return cudaMemsetAsync(ws, 0, sizeof(DeviceStatus), s) == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
-}
-
-float log2_scale(float sm_scale, int D) {
-  if (!(sm_scale > 0.0f)) sm_scale = (float)(1.0 / sqrt((double)D));
-  return (float)((double)sm_scale * 1.4426950408889634074);
 }
 
 // The SAGE_MAINLOOP environment variable picks the mainloop until the first
@@ -306,11 +259,13 @@ std::vector<int> host_chunks(int H, int hc) {
 extern "C" {
 
 int sage_workspace_bytes(int op, int B, int N, int H, int D, size_t* bytes) {
-  if (!bytes || op < SAGE_OP_QUANT_QK || op > SAGE_OP_ATTN_FWD_HOST) return SAGE_ERR_INVALID_ARG;
+  if (!bytes || op < SAGE_OP_QUANT_QK || op > SAGE_OP_CACHE_ATTN) return SAGE_ERR_INVALID_ARG;
   int rc = check_dims(B, N, H, D);
   if (rc) return rc;
   if (op == SAGE_OP_ATTN_FWD_HOST)  // two chunk workspaces of H heads
     *bytes = 2 * align_up(plan(SAGE_OP_ATTN_FWD, make_dims(B, N, H, D)).total);
+  else if (op == SAGE_OP_CACHE_ATTN)
+    *bytes = align_up(SAGE_STATUS_BYTES) + cache_attn_workspace_bytes();
   else
     *bytes = plan(op, make_dims(B, N, H, D)).total;
   return SAGE_OK;

@@ -98,8 +98,12 @@ enum sage_op {
   SAGE_OP_ATTN_FROM_QUANT = 3,
   SAGE_OP_DEBUG_QK = 4,
   SAGE_OP_QUANT_QKV = 5,
-  SAGE_OP_ATTN_FWD_HOST = 6  /* sage_attn_fwd_host with chunks of H heads and
+  SAGE_OP_ATTN_FWD_HOST = 6, /* sage_attn_fwd_host with chunks of H heads and
                                 two compute streams (two chunk workspaces) */
+  SAGE_OP_CACHE = 7,         /* sage_cache_append, sage_cache_read */
+  SAGE_OP_CACHE_ATTN = 8     /* sage_cache_attn (N: drafted tokens, H: Q heads);
+                                the same size for every shape, and enough for
+                                the other cache calls too */
 };
 
 /* Mainloop implementations.  DEFAULT, TCGEN05 and MMA_SYNC compute the
@@ -390,6 +394,144 @@ SAGE_API int sage_debug_qk_s32(const int8_t* q_i8, const float* q_scale, const i
                                const uint8_t* v_fp8, const float* v_scale, int B, int N, int H, int D, int b, int h,
                                int q_tile, int k_tile, int32_t* s_out, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * Serving: rotary positions, a quantised paged cache, and the attention of
+ * new or drafted tokens over it (no counterpart in the pages: the quantised
+ * tensors above are made anew by every call; these keep them between calls,
+ * one token at a time).  A step of a serving loop is sage_rope on the new Q
+ * and K, sage_cache_append, sage_cache_attn.
+ *
+ * The cache.  Every token has, per head, D codes of K and of V and one FP32
+ * scale for each; nothing is shared between tokens, so a token is appended
+ * without touching the others and its row may be copied to another slot.
+ * Pages hold page_size tokens; slot s of sequence b is row s % page_size of
+ * page page_table[b][s / page_size].  Sequences may share pages that are only
+ * read.  Page tables and lengths are device tensors, so that a captured graph
+ * follows them.
+ *
+ * Device checks.  A slot behind the table or an entry that names no page
+ * (below 0, or >= pages) is skipped: the token is not written, not read or
+ * not attended to, and SAGE_ERR_DEVICE goes to the status word.  So does a
+ * count below 0 (taken as 0) or above N (taken as N) and a start or context below 0.  Unlike the
+ * calls above, the cache calls do not clear the status word: zero the
+ * workspace's first SAGE_STATUS_BYTES once (sage_clear_device_status), then
+ * the word keeps the first error of all calls, and a loop or a replayed graph
+ * reads it once with sage_read_device_status.  Calls that can overlap need
+ * separate workspaces. */
+enum sage_cache_format {
+  SAGE_CACHE_INT8 = 0, /* round(x * 127 / amax) */
+  SAGE_CACHE_E4M3 = 1  /* E4M3 ("FN") of x * 448 / amax */
+};
+
+typedef struct sage_cache {
+  void* k_codes;  /* [pages][H][page_size][D], one byte each */
+  float* k_scale; /* [pages][H][page_size] */
+  void* v_codes;
+  float* v_scale;
+  int k_format, v_format; /* enum sage_cache_format */
+  int pages;
+  int page_size; /* 16, 32, 64 or 128; pages * H * page_size < 2^31 */
+  int H, D;
+} sage_cache;
+
+enum sage_rope_layout {
+  SAGE_ROPE_HALF = 0,       /* pair j: channels j and j + rot_dim/2 */
+  SAGE_ROPE_INTERLEAVED = 1 /* pair j: channels 2j and 2j + 1 */
+};
+
+/* Frequencies f_j = base^(-2j / rot_dim), stretched for contexts `factor`
+ * (>= 1) times as long as the trained one. */
+enum sage_rope_scaling {
+  SAGE_ROPE_PLAIN = 0,
+  SAGE_ROPE_LINEAR = 1, /* f_j / factor */
+  SAGE_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) */
+  SAGE_ROPE_YARN = 3    /* by parts: pairs of more than beta_fast turns over
+                           trained_len keep f_j, pairs of fewer than beta_slow
+                           get f_j / factor, with a linear ramp over j between;
+                           mscale = 0.1 ln(factor) + 1 */
+};
+
+typedef struct sage_rope_config {
+  int scaling; /* enum sage_rope_scaling */
+  int rot_dim; /* even, 2 .. 128 */
+  double base, factor;
+  double trained_len, beta_fast, beta_slow; /* SAGE_ROPE_YARN */
+} sage_rope_config;
+
+/* Host call, no GPU: the rot_dim/2 frequencies (FP64, radians per position)
+ * and the factor of the rotated channels, for sage_rope.  The caller copies
+ * inv_freq to the device.  SAGE_ERR_INVALID_ARG for a null pointer, base <= 1,
+ * factor < 1 or bad ramp limits; SAGE_ERR_UNSUPPORTED for the rot_dim. */
+SAGE_API int sage_rope_freqs(const sage_rope_config* config, double* inv_freq, float* mscale);
+
+/* Rotary positions on Q [B, N, Hq, D] and K [B, N, Hk, D] (either head count
+ * may be 0, its view and output then unused), in one launch:
+ *   a = position * inv_freq[j] (FP64),  c = mscale cos a,  s = mscale sin a,
+ *   (y0, y1) = bf16(x0 c - x1 s, x1 c + x0 s)   in FP32, rounded once,
+ * for the rot_dim/2 pairs of each head; channels from rot_dim on are copied.
+ *   - positions: device int32 [B][N] with row stride pos_stride_b (0: the same
+ *     for every b); NULL: 0 .. N-1.  inv_freq: device FP64 [rot_dim/2].
+ *   - inverse != 0 rotates by -a: the transpose, which is the gradient with
+ *     respect to the input for the gradient of the output.
+ *   - An output may be its input view itself (same base and strides); rows
+ *     must not overlap otherwise.
+ * No workspace.  rot_dim even, 2 .. D, else SAGE_ERR_UNSUPPORTED. */
+SAGE_API int sage_rope(sage_view_bf16 q, int Hq, void* q_out, int64_t q_out_stride_b, int64_t q_out_stride_n,
+                       int64_t q_out_stride_h, sage_view_bf16 k, int Hk, void* k_out, int64_t k_out_stride_b,
+                       int64_t k_out_stride_n, int64_t k_out_stride_h, const int32_t* positions,
+                       int64_t pos_stride_b, const double* inv_freq, float mscale, int layout, int rot_dim,
+                       int inverse, int B, int N, int D, void* stream);
+
+/* Quantise the first count[b] (NULL: N) tokens of K and V [B, N, H, D] into
+ * slots start[b], start[b]+1, ... (NULL: from 0) of each sequence.  Per row:
+ *   amax = max |x|,  scale = fl32(amax / top),  code = x * top / amax rounded
+ * once to the nearest code, ties to even (top = 127 or 448); a row of zeros
+ * has scale and codes 0; a row with an infinity or a NaN has scale NaN and
+ * codes 0.  start, count: device int32 [B].  The slots of one call must be
+ * distinct (a row that two tokens name is left in an undefined state).
+ * Workspace: sage_workspace_bytes(SAGE_OP_CACHE, ...). */
+SAGE_API int sage_cache_append(const sage_cache* cache, sage_view_bf16 k, sage_view_bf16 v, const int32_t* page_table,
+                               int table_pages, const int32_t* start, const int32_t* count, int B, int N,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The reverse: bf16(fl32(code * scale)) of slots start[b] .. start[b] +
+ * count[b] - 1 into rows 0 .. count[b]-1 of k_out and v_out [B, N, H, D]
+ * (either may be NULL).  The other rows are left as they were. */
+SAGE_API int sage_cache_read(const sage_cache* cache, const int32_t* page_table, int table_pages, const int32_t* start,
+                             const int32_t* count, void* k_out, int64_t k_out_stride_b, int64_t k_out_stride_n,
+                             int64_t k_out_stride_h, void* v_out, int64_t v_out_stride_b, int64_t v_out_stride_n,
+                             int64_t v_out_stride_h, int B, int N, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+#define SAGE_CACHE_MAX_DRAFT 256
+
+/* Attention of T (1 .. SAGE_CACHE_MAX_DRAFT) new or drafted tokens per
+ * sequence over the cache, which already holds them: token i of sequence b is
+ * in slot context[b] + i, and sees slots 0 .. context[b]-1 and those drafted
+ * tokens j whose bit (mask[b][i][j / 32] >> (j % 32)) & 1 is set (a tree: its
+ * ancestors and itself); mask NULL: j <= i.  With T = 1 this is a decode step.
+ *   - q, out: [B, T, Hq, D]; Hq a multiple of cache->H, and Q heads
+ *     h*G .. h*G + G-1 share head h of the cache, G = Hq / H.
+ *   - count[b] (NULL: T) tokens are drafted in sequence b; rows from count[b]
+ *     on are left as they were and bits of j >= count[b] are ignored.
+ *   - s_j = q . k_j * sm_scale (<= 0: 1/sqrt(D)) on the dequantised K, FP32
+ *     softmax statistics, out = bf16(sum softmax(s)_j v_j); the products are
+ *     of FP16 values, exact for the codes, with FP32 sums; a probability times
+ *     its V scale over a power of two at or above the row's largest V scale is
+ *     rounded to FP16 (V scales from 2^-60 to 2^75 keep that precision).
+ *   - lse (NULL or [B][T][Hq]): ln sum_j exp(s_j).
+ *   - A row that sees nothing: out 0, lse -inf.
+ * Masked and unused slots may hold any bytes.  Workspace:
+ * sage_workspace_bytes(SAGE_OP_CACHE_ATTN, ...). */
+SAGE_API int sage_cache_attn(sage_view_bf16 q, const sage_cache* cache, const int32_t* page_table, int table_pages,
+                             const int32_t* context, const int32_t* count, const uint32_t* mask, void* out,
+                             int64_t out_stride_b, int64_t out_stride_n, int64_t out_stride_h, float* lse, int B,
+                             int T, int Hq, float sm_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Zero the status word (and the rest of the first SAGE_STATUS_BYTES) of a
+ * workspace, on `stream`. */
+SAGE_API int sage_clear_device_status(void* workspace, void* stream);
 
 #ifdef __cplusplus
 }
