@@ -358,8 +358,7 @@ def sage_debug_prepass_list(B: int, N: int, H: int, D: int, grid: int):
     items = np.zeros((n, 3), dtype=np.int32)
     lag = ctypes.c_int(0)
     _check(lib().sage_debug_prepass_list(B, N, H, D, grid, ctypes.byref(lag), n, items.ctypes.data),
-           "sage_debug_prepass_list", "sage_rope_freqs", "sage_rope", "sage_cache_append", "sage_cache_read",
-           "sage_cache_attn", "sage_clear_device_status")
+           "sage_debug_prepass_list")
     return lag.value, items
 
 
