@@ -31,6 +31,7 @@ int check_table(const sage_cache* c, const int32_t* table, int table_pages, cons
                 void* ws, size_t ws_bytes, size_t need) {
   if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !table) return SAGE_ERR_INVALID_ARG;
   if (table_pages < 1) return SAGE_ERR_INVALID_ARG;
+  if ((int64_t)table_pages * c->page_size > (1 << 28)) return SAGE_ERR_UNSUPPORTED;
   if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
       !aligned4(table) || !aligned4(a) || !aligned4(b))
     return SAGE_ERR_UNSUPPORTED;

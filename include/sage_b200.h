@@ -405,7 +405,7 @@ SAGE_API int sage_debug_qk_s32(const int8_t* q_i8, const float* q_scale, const i
  * The cache.  Every token has, per head, D codes of K and of V and one FP32
  * scale for each; nothing is shared between tokens, so a token is appended
  * without touching the others and its row may be copied to another slot.
- * Pages hold page_size tokens; slot s of sequence b is row s % page_size of
+ * Pages hold page_size tokens (a sequence's table at most 2^28); slot s of sequence b is row s % page_size of
  * page page_table[b][s / page_size].  Sequences may share pages that are only
  * read.  Page tables and lengths are device tensors, so that a captured graph
  * follows them.
@@ -519,7 +519,7 @@ SAGE_API int sage_cache_read(const sage_cache* cache, const int32_t* page_table,
  *     softmax statistics, out = bf16(sum softmax(s)_j v_j); the products are
  *     of FP16 values, exact for the codes, with FP32 sums; a probability times
  *     its V scale over a power of two at or above the row's largest V scale is
- *     rounded to FP16 (V scales from 2^-60 to 2^75 keep that precision).
+ *     rounded to FP16.
  *   - lse (NULL or [B][T][Hq]): ln sum_j exp(s_j).
  *   - A row that sees nothing: out 0, lse -inf.
  * Masked and unused slots may hold any bytes.  Workspace:

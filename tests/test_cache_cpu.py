@@ -107,7 +107,7 @@ def test_append_and_read_refusals(lib):
         for bad, code in CACHE_BAD:
             if code:
                 assert call(c=cache_struct(**bad)) == code, bad
-        for bad, code in ((dict(table=None), 1), (dict(per=0), 1), (dict(table=4098), 2), (dict(start=4098), 2),
+        for bad, code in ((dict(table=None), 1), (dict(per=0), 1), (dict(per=(1 << 24) + 1), 2), (dict(table=4098), 2), (dict(start=4098), 2),
                           (dict(count=4098), 2), (dict(ws=None), 3), (dict(ws=4112), 3), (dict(n=100), 3),
                           (dict(B=-1), 1), (dict(N=-1), 1), (dict(B=70000), 2)):
             assert call(**bad) == code, bad
@@ -132,7 +132,7 @@ def test_attention_refusals(lib):
         if code:
             assert call(c=cache_struct(**bad)) == code, bad
     for bad, code in ((dict(q=NULL), 1), (dict(q=ODD), 2), (dict(q=STRIDE), 2), (dict(table=None), 1), (dict(per=0), 1),
-                      (dict(ctx=None), 1), (dict(ctx=4098), 2), (dict(count=4098), 2), (dict(mask=4098), 2),
+                      (dict(per=(1 << 24) + 1), 2), (dict(ctx=None), 1), (dict(ctx=4098), 2), (dict(count=4098), 2), (dict(mask=4098), 2),
                       (dict(lse=4098), 2), (dict(out=None), 1), (dict(out=4104), 2), (dict(so=-8), 1), (dict(Hq=3), 1),
                       (dict(Hq=-2), 1), (dict(T=257), 2), (dict(T=-1), 1), (dict(ws=None), 3), (dict(ws=4112), 3),
                       (dict(n=need - 1), 3), (dict(B=70000), 2), (dict(c=cache_struct(H=0)), 1)):

@@ -327,16 +327,31 @@ def test_attn_score_range(sage, ws, T, G):
 
 
 def test_attn_tiny_v_scales(sage, ws):
-    """V of small and large magnitudes (scales from 2^-60 to 2^75 keep their precision), alone and beside each other."""
-    context = [40, 40, 40]
+    """V of small and large magnitudes, alone and beside each other."""
+    context = [40] * 5
     cache, table = filled(sage, [n + 1 for n in context], 1, 16, 64, INT8, INT8, seed=3)
     vs = cache[3]
-    for b, (lo, hi) in enumerate(((1e-18, 1e-18), (3e22, 3e22), (1e-12, 1e12))):
+    for b, (lo, hi) in enumerate(((1e-18, 1e-18), (3e22, 3e22), (1e-12, 1e12), (1e-36, 1e-36), (1e34, 1e-34))):
         for s in range(41):
             vs[int(table[b, s // 16]), 0, s % 16] = lo if s % 2 else hi
-    q = rand(3, 1, 4, 64, seed=4)
+    q = rand(5, 1, 4, 64, seed=4)
     out, lse = run_attn(sage, ws, q, cache, table, i32(*context), None, None)
     check_attn(q, cache, table, i32(*context), None, None, out, lse)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (20, 8)])
+def test_attn_hidden_draft_of_huge_values(sage, ws, T, G):
+    """A drafted token that a row does not see may hold any V: the row keeps its precision."""
+    T += 1
+    context = [70]
+    cache, table = filled(sage, [70 + T], 1, 16, 64, INT8, E4M3, seed=31)
+    big = rand(1, 1, 1, 64, seed=32) * 2.0 ** 100
+    sage.sage_cache_append(cache, big, big, table, i32(70 + T - 1), None, ws)
+    mask = cu.tree_mask([[i - 1 for i in range(T - 1)] + [-1]], DEV)
+    q = rand(1, T, G, 64, seed=33)
+    out, lse = run_attn(sage, ws, q, cache, table, i32(*context), None, mask)
+    check_attn(q[:, :T - 1], cache, table, i32(*context), None, cu.tree_mask([[i - 1 for i in range(T - 1)]], DEV),
+               out[:, :T - 1], lse[:, :T - 1])
 
 
 @pytest.mark.parametrize("T,G", [(1, 4), (24, 8)])
