@@ -5,25 +5,29 @@
 //   s_j = (q . k_j) * kscale_j * sm_scale,  out = sum_j softmax(s)_j v_j vscale_j,
 //   lse = ln sum_j exp(s_j);  a row that sees nothing has out = 0, lse = -inf.
 //
-// The count*G rows that share a head of the cache are the M side of
-// m16n8k16 FP16 MMAs with FP32 sums, MT tiles of 16 rows at a time, so that
-// every code is read and converted once for all of them.  The codes are exact
-// in FP16.  Q is FP16 too: a row is scaled by a power of two that brings its
-// largest value to 2^13, which leaves its BF16 values exact down to 2^-27 of
-// the largest.
+// Transposed products: S^T = K Q^T and O^T = V^T P^T as m16n8k16 FP16 MMAs
+// with FP32 sums, the codes (exact in FP16) as the A operand and NT groups of 8
+// of the count*G rows that share a head as the B operand, so that a decode step
+// of up to 8 query heads per head wastes no MMA and every code is read and
+// converted once for all rows.  Q is FP16 too: a row is scaled by a power of two
+// that brings its largest value to 2^13, which leaves its BF16 values exact
+// down to 2^-27 of the largest.
 //
-// Online softmax per row in base 2 with the running maximum c: FP32 sums
-// l += p_j and O += w_j code_j, p_j = 2^(s_j - c) and w_j = p_j vscale_j 2^-E
-// rounded to FP16 (2^-11) for the PV MMA.  E is an integer per row with 2^E
-// at or above the largest V scale that the row has seen, so that w_j is at most
-// 1; it is per row because a token that only other rows see may have any scale.
+// Online softmax per row in base 2: FP32 sums l += p_j and O += w_j code_j,
+// p_j = 2^(s_j - c) and w_j = p_j vscale_j 2^-E rounded to FP16 (2^-11).  The
+// offset c is the largest score at the row's last update and is raised only when
+// a score passes it by more than 8 (so p_j <= 2^8), which one vote per tile finds
+// out: later tiles need no reduction across lanes.  E is an integer per row with
+// 2^E at or above the largest V scale that the row has seen; it is per row
+// because a token that only other rows see may have any scale.
 //
-// Eight warps per CTA, one CTA per SM.  A warp takes every eighth tile of 16
-// keys of the CTA's stretch of the work list and runs alone: lane 0 keeps its
-// ring of K and V tiles (2 KB each at D = 128) filled by TMA, several tiles
-// ahead and across units, and the warps meet only where a unit ends, to join
-// their rows in shared memory.  16 keys are the smallest page, so a tile never
-// crosses one.
+// One CTA per SM.  A CTA's stretch of the work list is cut once more, into one
+// stretch per warp, and the warps run alone: lane 0 keeps its ring of K and V
+// tiles of 32 keys filled by TMA, ahead and across units; a unit that lies
+// within the warp's stretch is finished from its registers, one that is cut
+// leaves a part in the workspace, and the CTA joins its warps' parts once, at its
+// end.  A tile is two boxes of 16 keys, the smallest page, so a box never crosses
+// one.
 #include "cache_attn.cuh"
 #include "tc_prims.cuh"
 
@@ -32,14 +36,12 @@ namespace {
 
 using namespace cattn;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;       // keys
-constexpr int kMaxCtas = 148;   // one per SM
+constexpr int kTile = 32, kBox = 16;  // keys
+constexpr float kRaise = 8.0f;
 
-// n index of an 8-key MMA tile -> key.  Keys of neighbouring n differ in bits
-// 0 and 2, so the 16-byte shared-memory reads of two rows fall on different
-// banks under both swizzles (64- and 128-byte rows).
+// Row of an 8-key block of an MMA operand -> key.  Keys of neighbouring rows
+// differ in bits 0 and 2, so the 16-byte shared-memory reads of two rows fall
+// on different banks under both swizzles (64- and 128-byte rows).
 __device__ __forceinline__ int key_of(int n) { return (n >> 1) ^ ((n & 1) ? 5 : 0); }
 
 // Four codes -> bytes 0 and 2, and bytes 1 and 3, as FP16 pairs.
@@ -73,11 +75,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -86,445 +97,499 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Two FP32 values in one 64-bit register (a row pair).
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 template <int D>
 __device__ __forceinline__ uint32_t swizzled(int key, int chunk) {
   return key * D + ((D == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3)) << 4);
 }
 
-template <int D, int MT>
+// Launch shape by the number of 8-row groups.
+template <int D, int NT>
+struct Shape {
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (kWarps == 12 ? 2 : 3);
+};
+
+// The last unit of a warp's stretch, and the first of the CTA's: what the CTA's
+// join needs of it.  slot -1: the warp left no such part.
+struct Cut {
+  long long start, end;  // of the unit, in the list
+  int slot, b, h, row0, rows;
+};
+
+template <int D, int NT>
 struct Smem {
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kFrags = MT * (D / 8) * 4;  // FP32 sums per lane
-  alignas(1024) uint8_t k[kWarps][kStages][kTile * D];
-  alignas(1024) uint8_t v[kWarps][kStages][kTile * D];
-  float join[kWarps / 2][kFrags][32];
-  uint4 q[MT > 1 ? MT : 1][D / 16][32];  // MT > 1: Q fragments
-  float f[16 * MT];
-  float c[kWarps][16 * MT], l[kWarps][16 * MT];
-  uint64_t full[kWarps][kStages];
+  using Sh = Shape<D, NT>;
+  alignas(1024) uint8_t k[Sh::kWarps][Sh::kStages][kTile * D];
+  alignas(1024) uint8_t v[Sh::kWarps][Sh::kStages][kTile * D];
+  float c[Sh::kWarps][2][8 * NT], l[Sh::kWarps][2][8 * NT];  // of the parts
+  Cut cut[Sh::kWarps + 1];  // [w]: a unit that begins in warp w's stretch and goes on; [kWarps]: one that began before the CTA's
+  uint64_t full[Sh::kWarps][Sh::kStages];
   StretchSmem stretch;
 };
 
-// Running state of the thread's two rows (g and g + 8) of one 16-row tile.
+// Running state of the thread's rows 8 nt + 2c and 8 nt + 2c + 1.
 struct Rows {
-  float M[2], c[2], l[2];
-  int E[2];
+  uint64_t l, f, nc, down;  // pairs: sum, score factor, -c, 2^-E
+  float thr[2];             // raw score above which c is raised; -inf: nothing seen yet
 };
 
-template <int D, int MT, int KF, int VF>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NT, int KF, int VF>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     cache_attn_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const CacheAttnArgs a) {
-  constexpr int R = 16 * MT, KS = D / 16;  // rows of a unit, k steps of QK
-  constexpr int S = Smem<D, MT>::kStages;
+  using Sh = Shape<D, NT>;
+  constexpr int R = 8 * NT, KS = D / 16, S = Sh::kStages, W = Sh::kWarps, XV = D / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D, MT>& sm = *reinterpret_cast<Smem<D, MT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
 
-  if (threadIdx.x < kWarps * S) tc::mbar_init(&sm.full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x <= W) sm.cut[threadIdx.x].slot = -1;
+  if (threadIdx.x < W * S) tc::mbar_init(&sm.full[0][0] + threadIdx.x, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0)  // lengths that cannot be
-    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+    for (int b = threadIdx.x; b < a.B; b += Sh::kThreads) {
       const int ctx = a.context[b], cnt = a.count ? a.count[b] : a.T;
       if (ctx < 0 || cnt < 0 || cnt > a.T ||
           (long long)ctx + cnt > ((long long)a.c.table_pages << a.c.page_shift))
         flag_bad(a.c.status, kWhereAttn);
     }
-  const Stretch st = find_stretch<kTile, R, kThreads, kWarps>(a, blockIdx.x, gridDim.x, sm.stretch);
+  const Stretch st = find_stretch<kTile, R, Sh::kThreads, W>(a, blockIdx.x, gridDim.x, sm.stretch);
   __syncthreads();
   if (st.s >= st.e) return;
 
-  // ---- this warp's tiles: list indices first, first + 8, ...; nt of them
-  const long long first = st.s + warp;
-  const int nt = first < st.e ? (int)((st.e - first + kWarps - 1) / kWarps) : 0;
-  // cache rows (of head h, from the tile's first key on) of tiles 32 blk + lane: this block of 32 and the next
+  // ---- this warp's tiles: list indices [first, last)
+  const long long share = st.share / W, first = min(st.s + warp * share, st.e), last = min(first + share, st.e);
+  const int n_tiles = (int)(last - first);
+  // cache rows of the two boxes of tiles 32 blk + lane, -1 for a box without keys: this block of 32 tiles and the next
   Place walk = st.p;
-  auto rows_of_block = [&](int blk) -> int {
-    const long long idx = first + (long long)kWarps * (32 * blk + lane);
-    if (idx >= st.e) return -1;
+  auto rows_of_block = [&](int blk, int& r0, int& r1) {
+    r0 = r1 = -1;
+    const long long idx = first + 32 * blk + lane;
+    if (idx >= last) return;
     go_to<kTile, R>(a, walk, idx);
     const Unit u = unit_of(walk, idx);
-    const int64_t row = cache_row(a.c, walk.b, u.h, (idx - u.start) * kTile);
-    if (row < 0) flag_bad(a.c.status, kWhereAttn);
-    return (int)row;
-  };
-  int block = 0, rows_a = rows_of_block(0), rows_b = nt > 32 ? rows_of_block(1) : -1;
-  auto row_of = [&](int i) { return __shfl_sync(0xffffffffu, (i >> 5) == block ? rows_a : rows_b, i & 31); };
-  auto issue = [&](int i) {
-    const int row = row_of(i), s = i % S;
-    if (row >= 0 && lane == 0) {
-      tc::mbar_expect_tx(&sm.full[warp][s], 2 * kTile * D);
-      tc::tma_load_3d(sm.k[warp][s], &tm_k, 0, row, 0, &sm.full[warp][s]);
-      tc::tma_load_3d(sm.v[warp][s], &tm_v, 0, row, 0, &sm.full[warp][s]);
+    const int64_t slot = (idx - u.start) * kTile, end = (int64_t)walk.s.ctx + walk.s.cnt;
+    r0 = (int)cache_row(a.c, walk.b, u.h, slot);
+    if (r0 < 0) flag_bad(a.c.status, kWhereAttn);
+    if (slot + kBox < end) {
+      r1 = (int)cache_row(a.c, walk.b, u.h, slot + kBox);
+      if (r1 < 0) flag_bad(a.c.status, kWhereAttn);
     }
   };
-  // the tile's K scales in lanes 0-15, its V scales in lanes 16-31
-  auto scales_of = [&](int i) -> float {
-    const int row = row_of(i);
-    return row < 0 ? 0.0f : __ldg(lane < 16 ? a.c.scale[0] + row + lane : a.c.scale[1] + row + (lane - 16));
+  int block = 0, ra0, ra1, rb0 = -1, rb1 = -1;
+  rows_of_block(0, ra0, ra1);
+  if (n_tiles > 32) rows_of_block(1, rb0, rb1);
+  auto row0_of = [&](int i) { return __shfl_sync(0xffffffffu, (i >> 5) == block ? ra0 : rb0, i & 31); };
+  auto row1_of = [&](int i) { return __shfl_sync(0xffffffffu, (i >> 5) == block ? ra1 : rb1, i & 31); };
+  auto issue = [&](int i) {
+    const int r0 = row0_of(i), r1 = row1_of(i), s = i % S;
+    if (lane == 0 && (r0 >= 0 || r1 >= 0)) {
+      uint64_t* bar = &sm.full[warp][s];
+      tc::mbar_expect_tx(bar, (r0 >= 0 && r1 >= 0 ? 4 : 2) * kBox * D);
+      if (r0 >= 0) {
+        tc::tma_load_3d(sm.k[warp][s], &tm_k, 0, r0, 0, bar);
+        tc::tma_load_3d(sm.v[warp][s], &tm_v, 0, r0, 0, bar);
+      }
+      if (r1 >= 0) {
+        tc::tma_load_3d(sm.k[warp][s] + kBox * D, &tm_k, 0, r1, 0, bar);
+        tc::tma_load_3d(sm.v[warp][s] + kBox * D, &tm_v, 0, r1, 0, bar);
+      }
+    }
   };
-  int issued = min(S, nt);
+  // the scales of the tile's key `lane`
+  auto scales_of = [&](int i, float& ks, float& vs) {
+    const int r0 = row0_of(i), r1 = row1_of(i), row = lane < kBox ? r0 : r1;
+    ks = row < 0 ? 0.0f : __ldg(a.c.scale[0] + row + (lane & 15));
+    vs = row < 0 ? 0.0f : __ldg(a.c.scale[1] + row + (lane & 15));
+  };
+  int issued = min(S, n_tiles);
   for (int i = 0; i < issued; ++i) issue(i);
-  float sc_next = nt > 0 ? scales_of(0) : 0.0f;
+  float ks_next = 0.0f, vs_next = 0.0f;
+  if (n_tiles > 0) scales_of(0, ks_next, vs_next);
   uint32_t phase = 0;
   bool dead = false;  // a TMA tile that never came: nothing more is issued or computed
   int abort_flag = 0;
 
   const uint32_t kbase = smem_u32(sm.k[warp][0]), vbase = smem_u32(sm.v[warp][0]);
-  const int vkey = 8 * ((lane >> 3) & 1) + key_of(lane & 7), vchunk = lane >> 4;  // this lane's ldmatrix row
+  // this lane's 16-byte reads: K row key_of(g), V row of its ldmatrix matrix
+  const uint32_t ksw = swizzled<D>(key_of(g), c4);
+  const int vkey = 8 * ((lane >> 3) & 1) + key_of(lane & 7), vchunk = lane >> 4;
 
   Place at = st.p;
   int i = 0;
-  for (long long seg = st.s; seg < st.e;) {
+  for (long long seg = first; seg < last;) {
     go_to<kTile, R>(a, at, seg);
     const Unit u = unit_of(at, seg);
     const int b = at.b, h = u.h, row0 = u.rt * R;
     const int ctx = at.s.ctx, cnt = at.s.cnt, rows = min(R, cnt * a.G - row0);
-    const long long unit_end = u.start + at.s.n, seg_end = min(unit_end, st.e);
-    const int i_end = seg_end > first ? (int)((seg_end - first + kWarps - 1) / kWarps) : 0;
+    const long long unit_end = u.start + at.s.n, seg_end = min(unit_end, last);
+    const int i_end = (int)(seg_end - first);
 
-    // ---- Q rows as A fragments: of k step 4x + i, k = 2c, 2c+1 and 2c+8, 2c+9 are channels 64x + 16c + 4i + 0, 2
+    // ---- Q rows as B fragments: of k step 4x + y, k = 2c, 2c+1 and 2c+8, 2c+9 are channels 64x + 16c + 4y + 0, 2
     // and + 1, 3, the bytes 0, 2 and 1, 3 of the K words
-    uint32_t qf[MT == 1 ? KS : 1][4];
-    float f[MT][2];
-    auto load_q = [&](int mt, auto&& put) {
-      uint32_t w[2][D / 8];
+    uint2 qf[NT][KS];
+    Rows rs[NT];
+    auto load_q = [&](int nt, auto&& put) -> float {
+      uint32_t w[D / 8];
+      const int lr = 8 * nt + g;
+      const int t = (row0 + lr) / a.G, hq = h * a.G + (row0 + lr) % a.G;
+      const uint16_t* q = a.q + b * a.qb + t * a.qn + hq * a.qh + 16 * c4;
+      uint32_t top = 0;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int lr = 16 * mt + g + 8 * r;
-        const bool on = lr < rows;
-        const int t = (row0 + lr) / a.G, hq = h * a.G + (row0 + lr) % a.G;
-        const uint16_t* q = a.q + b * a.qb + t * a.qn + hq * a.qh + 16 * c4;
-        uint32_t top = 0;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (on) v = __ldg(reinterpret_cast<const uint4*>(q + 64 * x + 8 * y));
-            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[r][8 * x + 4 * y + e] = vw[e];
-              top = max(top, max(vw[e] & 0x7FFFu, (vw[e] >> 16) & 0x7FFFu));
-            }
-          }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int eq = (top == 0 || top >= 0x7F80u) ? 0 : max((int)(top >> 7) - 127 - 13, -110);
-        const float down = __int_as_float((127 - eq) << 23);
-        f[mt][r] = fmaxf(a.sl2 * __int_as_float((127 + eq) << 23), 1.17549435e-38f);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const uint32_t w0 = w[r][2 * s], w1 = w[r][2 * s + 1];  // channels 4s .. 4s + 3 of this lane's
-          put(s, r, pack_f16x2(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down),
-              pack_f16x2(__uint_as_float(w0 & 0xFFFF0000u) * down, __uint_as_float(w1 & 0xFFFF0000u) * down));
-        }
-      }
-    };
-    if constexpr (MT == 1) {
-      load_q(0, [&](int s, int r, uint32_t even, uint32_t odd) { qf[s][r] = even; qf[s][2 + r] = odd; });
-    } else {
-      if (warp < MT) {
-        load_q(warp % MT, [&](int s, int r, uint32_t even, uint32_t odd) {
-          uint32_t* to = reinterpret_cast<uint32_t*>(&sm.q[warp % MT][s][lane]);
-          to[r] = even;
-          to[2 + r] = odd;
-        });
-      }
-    }
-    float o[MT][D / 8][4];
-    Rows rs[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        rs[mt].M[r] = -INFINITY;
-        rs[mt].c[r] = 0.0f;
-        rs[mt].l[r] = 0.0f;
-        rs[mt].E[r] = -126;
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
-    }
-    if constexpr (MT > 1) {
-      if (warp < MT && c4 == 0) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          if (mt == warp) { sm.f[16 * mt + g] = f[mt][0]; sm.f[16 * mt + g + 8] = f[mt][1]; }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) { f[mt][0] = sm.f[16 * mt + g]; f[mt][1] = sm.f[16 * mt + g + 8]; }
-    }
-
-    // ---- one tile of 16 keys from slot `slot0` on
-    auto tile = [&](auto masked_tag, uint32_t ks_addr, uint32_t vs_addr, float sc, int64_t slot0) {
-      constexpr bool MASKED = decltype(masked_tag)::value;
-      float s[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.0f;
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
-        uint4 kw[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) kw[j] = lds128(ks_addr + swizzled<D>(8 * j + key_of(g), 4 * x + c4));
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t qa[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (MT == 1) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) qa[mt][e] = qf[4 * x + y][e];
-            } else {
-              const uint4 v = sm.q[mt][4 * x + y][lane];
-              qa[mt][0] = v.x; qa[mt][1] = v.y; qa[mt][2] = v.z; qa[mt][3] = v.w;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t w = y == 0 ? kw[j].x : y == 1 ? kw[j].y : y == 2 ? kw[j].z : kw[j].w;
-            uint32_t b0, b1;
-            codes_to_f16<KF>(w, b0, b1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][j], qa[mt], b0, b1);
-          }
-        }
-      }
-      float ksc[2][2], vsc[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = 8 * j + (e ? c4 ^ 5 : c4);
-          ksc[j][e] = __shfl_sync(0xffffffffu, sc, key);
-          vsc[j][e] = __shfl_sync(0xffffffffu, sc, 16 + key);
-        }
-      uint32_t pa[MT][4];
-      float al[MT][2];
-      bool moved = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        Rows& q = rs[mt];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x[2][2], vv[2][2];
-          float top = -INFINITY, vmax = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x[j][e] = s[mt][j][2 * r + e] * ksc[j][e];
-              vv[j][e] = vsc[j][e];
-              if (MASKED) {
-                const int64_t slot = slot0 + 8 * j + (e ? c4 ^ 5 : c4);
-                bool seen = slot < ctx;
-                const int lr = 16 * mt + g + 8 * r;
-                if (!seen && slot < (int64_t)ctx + cnt && lr < rows) {
-                  const int d = (int)(slot - ctx), t = (row0 + lr) / a.G;
-                  seen = a.mask ? (__ldg(a.mask + ((int64_t)b * a.T + t) * ((a.T + 31) / 32) + d / 32) >> (d % 32)) & 1u
-                                : d <= t;
-                }
-                if (!seen) { x[j][e] = -INFINITY; vv[j][e] = 0.0f; }
-              }
-              top = fmaxf(top, x[j][e]);
-              vmax = fmaxf(vmax, vv[j][e]);
-            }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-          const float M = fmaxf(q.M[r], top);
-          const int E = min(max(q.E[r], (__float_as_int(vmax) >> 23) - 126), 126);
-          const float c = M == -INFINITY ? 0.0f : M * f[mt][r], down = __int_as_float((127 - E) << 23);
-          const float al_l = q.M[r] == -INFINITY ? 0.0f : ex2f(q.c[r] - c);
-          al[mt][r] = E == q.E[r] ? al_l : al_l * ex2f((float)(q.E[r] - E));
-          moved |= al[mt][r] != 1.0f;
-          float w[2][2], sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p = ex2f(fmaf(x[j][e], f[mt][r], -c));
-              sum += p;
-              w[j][e] = p * (vv[j][e] * down);
-            }
-          q.l[r] = q.l[r] * al_l + sum;
-          q.M[r] = M; q.E[r] = E; q.c[r] = c;
-          pa[mt][r] = pack_f16x2(w[0][0], w[0][1]);
-          pa[mt][2 + r] = pack_f16x2(w[1][0], w[1][1]);
-        }
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][n][e] *= al[mt][e >> 1];
-      }
-#pragma unroll
-      for (int x = 0; x < D / 16; x += 2) {
-        uint32_t vw[4];
-        ldmatrix_x4_trans(vs_addr + swizzled<D>(vkey, x + vchunk), vw);
+      for (int x = 0; x < D / 64; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          uint32_t e0, o0, e1, o1;
-          codes_to_f16<VF>(MASKED ? no_nan<VF>(vw[2 * y]) : vw[2 * y], e0, o0);
-          codes_to_f16<VF>(MASKED ? no_nan<VF>(vw[2 * y + 1]) : vw[2 * y + 1], e1, o1);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (lr < rows) v = __ldg(reinterpret_cast<const uint4*>(q + 64 * x + 8 * y));
+          const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(o[mt][2 * (x + y)], pa[mt], e0, e1);
-            mma16816(o[mt][2 * (x + y) + 1], pa[mt], o0, o1);
+          for (int e = 0; e < 4; ++e) {
+            w[8 * x + 4 * y + e] = vw[e];
+            top = max(top, max(vw[e] & 0x7FFFu, (vw[e] >> 16) & 0x7FFFu));
+          }
+        }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int eq = (top == 0 || top >= 0x7F80u) ? 0 : max((int)(top >> 7) - 127 - 13, -110);
+      const float down = __int_as_float((127 - eq) << 23);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const uint32_t w0 = w[2 * s], w1 = w[2 * s + 1];
+        put(s, make_uint2(pack_f16x2(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down),
+                          pack_f16x2(__uint_as_float(w0 & 0xFFFF0000u) * down, __uint_as_float(w1 & 0xFFFF0000u) * down)));
+      }
+      return fmaxf(a.sl2 * __int_as_float((127 + eq) << 23), 1.17549435e-38f);
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float f = load_q(nt, [&](int s, uint2 v) { qf[nt][s] = v; });
+      rs[nt].f = pair(__shfl_sync(0xffffffffu, f, 8 * c4), __shfl_sync(0xffffffffu, f, 8 * c4 + 4));
+    }
+    float o[NT][XV][4];
+    float vlim = 1.17549435e-38f;  // the smallest 2^E of the thread's rows
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      rs[nt].l = rs[nt].nc = 0;
+      rs[nt].down = pair(0x1p126f, 0x1p126f);
+      rs[nt].thr[0] = rs[nt].thr[1] = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < XV; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][x][e] = 0.0f;
+    }
+
+    // ---- one tile of 32 keys from slot `slot0` on; box0, box1: it holds the keys of that box
+    auto tile = [&](auto masked_tag, uint32_t ka, uint32_t va, float ks, float vs, int64_t slot0, bool box0, bool box1) {
+      constexpr bool MASKED = decltype(masked_tag)::value;
+      float s[2][NT][4];  // keys 16 hf + key_of(g), + 8; rows 2c, 2c + 1
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[hf][nt][e] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        uint4 kw[2][2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) kw[hf][j] = lds128((ka + (16 * hf + 8 * j) * D + ksw) ^ (64 * x));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t fa[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint4& k4 = kw[hf][j];
+              codes_to_f16<KF>(y == 0 ? k4.x : y == 1 ? k4.y : y == 2 ? k4.z : k4.w, fa[j], fa[2 + j]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(s[hf][nt], fa, qf[nt][4 * x + y].x, qf[nt][4 * x + y].y);
           }
         }
       }
+      float vsc[2][2], vtop = 0.0f;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int key = 16 * hf + 8 * j + key_of(g);
+          const float kk = __shfl_sync(0xffffffffu, ks, key);
+          vsc[hf][j] = __shfl_sync(0xffffffffu, vs, key);
+          vtop = fmaxf(vtop, vsc[hf][j]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 x = unpair(mul2(pair(s[hf][nt][2 * j], s[hf][nt][2 * j + 1]), pair(kk, kk)));
+            s[hf][nt][2 * j] = x.x;
+            s[hf][nt][2 * j + 1] = x.y;
+          }
+        }
+      // a masked tile: which of its scores the rows see
+      uint32_t seen = 0xFFFFFFFFu;  // bit (nt * 8 + hf * 4 + j * 2 + e)
+      if (MASKED) {
+        seen = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * nt + 2 * c4 + e, t = (row0 + lr) / a.G;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int64_t slot = slot0 + 16 * hf + 8 * j + key_of(g);
+                bool on = slot < ctx;
+                if (!on && slot < (int64_t)ctx + cnt && lr < rows) {
+                  const int d = (int)(slot - ctx);
+                  on = a.mask ? (__ldg(a.mask + ((int64_t)b * a.T + t) * ((a.T + 31) / 32) + d / 32) >> (d % 32)) & 1u
+                              : d <= t;
+                }
+                if (on && (hf ? box1 : box0)) seen |= 1u << (nt * 8 + hf * 4 + j * 2 + e);
+                else s[hf][nt][2 * j + e] = -INFINITY;
+              }
+          }
+      }
+      bool up = MASKED || vtop > vlim;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          up |= fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e])) > rs[nt].thr[e];
+      if (__any_sync(0xffffffffu, up)) {
+        vlim = INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al_o[2], al_l[2], nc[2], dn[2];
+          const float2 f = unpair(rs[nt].f), nc_old = unpair(rs[nt].nc), dn_old = unpair(rs[nt].down);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY, vm = 0.0f;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                top = fmaxf(top, s[hf][nt][2 * j + e]);
+                if ((seen >> (nt * 8 + hf * 4 + j * 2 + e)) & 1u) vm = fmaxf(vm, vsc[hf][j]);
+              }
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
+            }
+            const float fe = e ? f.y : f.x, c_old = -(e ? nc_old.y : nc_old.x);
+            const bool none = rs[nt].thr[e] == -INFINITY;
+            const float c = none ? (top == -INFINITY ? 0.0f : top * fe) : fmaxf(c_old, top * fe);
+            al_l[e] = none ? 0.0f : ex2f(c_old - c);
+            if (top != -INFINITY && (none || c > c_old)) rs[nt].thr[e] = top + kRaise / fe;
+            const float d_old = e ? dn_old.y : dn_old.x;
+            const int E_old = 127 - (__float_as_int(d_old) >> 23);
+            const int E = min(max(E_old, (__float_as_int(vm) >> 23) - 126), 126);
+            dn[e] = __int_as_float((127 - E) << 23);
+            al_o[e] = E == E_old ? al_l[e] : al_l[e] * ex2f((float)(E_old - E));
+            nc[e] = -c;
+            vlim = fminf(vlim, __int_as_float((127 + E) << 23));
+          }
+          rs[nt].nc = pair(nc[0], nc[1]);
+          rs[nt].down = pair(dn[0], dn[1]);
+          rs[nt].l = mul2(rs[nt].l, pair(al_l[0], al_l[1]));
+#pragma unroll
+          for (int x = 0; x < XV; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][x][e] *= al_o[e & 1];
+        }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 x = unpair(fma2(pair(s[hf][nt][2 * j], s[hf][nt][2 * j + 1]), rs[nt].f, rs[nt].nc));
+            const uint64_t p = pair(ex2f(x.x), ex2f(x.y));
+            rs[nt].l = add2(rs[nt].l, p);
+            const float2 w = unpair(mul2(p, mul2(pair(vsc[hf][j], vsc[hf][j]), rs[nt].down)));
+            if (MASKED) {
+              const uint32_t on = seen >> (nt * 8 + hf * 4 + j * 2);
+              pb[hf][nt][j] = transpose8x8(pack_f16x2(on & 1u ? w.x : 0.0f, on & 2u ? w.y : 0.0f));
+            } else {
+              pb[hf][nt][j] = transpose8x8(pack_f16x2(w.x, w.y));
+            }
+          }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int x = 0; x < XV; x += 2) {
+          uint32_t vw[4];
+          ldmatrix_x4_trans(va + 16 * hf * D + swizzled<D>(vkey, x + vchunk), vw);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            uint32_t fa[4];
+            codes_to_f16<VF>(MASKED ? no_nan<VF>(vw[2 * y]) : vw[2 * y], fa[0], fa[1]);
+            codes_to_f16<VF>(MASKED ? no_nan<VF>(vw[2 * y + 1]) : vw[2 * y + 1], fa[2], fa[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][x + y], fa, pb[hf][nt][0], pb[hf][nt][1]);
+          }
+        }
     };
 
     for (; i < i_end; ++i) {
-      const int row = row_of(i), s = i % S;
-      const float sc = sc_next;
-      if (i + 1 < nt) sc_next = scales_of(i + 1);
-      if (row >= 0 && i < issued) {
+      const int r0 = row0_of(i), r1 = row1_of(i), s = i % S;
+      const float ks = ks_next, vs = vs_next;
+      if (i + 1 < n_tiles) scales_of(i + 1, ks_next, vs_next);
+      if ((r0 >= 0 || r1 >= 0) && i < issued) {
         if (!tc::wait_bounded(&sm.full[warp][s], (phase >> s) & 1u, &abort_flag, a.c.status, kWhereAttn,
                               kDefaultWaitLimit, false))
           dead = true;
         phase ^= 1u << s;
         dead = __any_sync(0xffffffffu, dead);
         if (!dead) {
-          const int64_t slot0 = (first + (long long)kWarps * i - u.start) * kTile;
+          const int64_t slot0 = (first + i - u.start) * kTile;
           const uint32_t ka = kbase + s * kTile * D, va = vbase + s * kTile * D;
-          if (slot0 + kTile <= ctx) tile(std::false_type{}, ka, va, sc, slot0);
-          else tile(std::true_type{}, ka, va, sc, slot0);
+          if (slot0 + kTile <= ctx && r0 >= 0 && r1 >= 0) tile(std::false_type{}, ka, va, ks, vs, slot0, true, true);
+          else tile(std::true_type{}, ka, va, ks, vs, slot0, r0 >= 0, r1 >= 0);
         }
       }
       __syncwarp();
-      if (issued < nt && !dead) issue(issued++);
+      if (issued < n_tiles && !dead) issue(issued++);
       if ((i & 31) == 31) {
         ++block;
-        rows_a = rows_b;
-        rows_b = nt > 32 * (block + 1) ? rows_of_block(block + 1) : -1;
+        ra0 = rb0;
+        ra1 = rb1;
+        if (n_tiles > 32 * (block + 1)) rows_of_block(block + 1, rb0, rb1);
       }
     }
 
-    // ---- join the warps' rows
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float l = rs[mt].l[r];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (c4 == 0) {
-          sm.c[warp][16 * mt + g + 8 * r] = rs[mt].M[r] == -INFINITY ? -INFINITY : rs[mt].c[r];
-          sm.l[warp][16 * mt + g + 8 * r] = l;
-        }
-      }
-    __syncthreads();
-    float cmax[MT][2], lsum[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int lr = 16 * mt + g + 8 * r;
-        float c = -INFINITY, l = 0.0f, mine = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) c = fmaxf(c, sm.c[w][lr]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float cw = sm.c[w][lr], fw = cw == -INFINITY ? 0.0f : ex2f(cw - c);
-          l += sm.l[w][lr] * fw;
-          if (w == warp) mine = fw;
-        }
-        cmax[mt][r] = c;
-        lsum[mt][r] = l;
-        mine *= __int_as_float((127 + rs[mt].E[r]) << 23);
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[mt][n][2 * r] *= mine;
-          o[mt][n][2 * r + 1] *= mine;
-        }
-      }
-    if (warp >= kWarps / 2) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sm.join[warp - kWarps / 2][(mt * (D / 8) + n) * 4 + e][lane] = o[mt][n][e];
-    }
-    __syncthreads();
-    if (warp < kWarps / 2) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sm.join[warp][(mt * (D / 8) + n) * 4 + e][lane] += o[mt][n][e];
-    }
-    __syncthreads();
+    // ---- the unit's rows, or this warp's part of them
     const bool whole = seg == u.start && seg_end == unit_end;
-    float* part = part_of<R, D>(a, blockIdx.x, seg == u.start ? 1 : 0);
-    // 16 columns of 16 rows at a time: even columns in fragment 2x, odd ones in 2x + 1
+    const int slot = seg == u.start ? 1 : 0;
+    float* part = warp_part<R, D>(a, blockIdx.x * W + warp, slot);
 #pragma unroll
-    for (int it = 0; it < (MT * D / 16 + kWarps - 1) / kWarps; ++it) {
-      const int item = it * kWarps + warp;
-      if (item < MT * D / 16) {
-        const int mt = item / (D / 16), x = item % (D / 16);
-        float v[2][4];
+    for (int nt = 0; nt < NT; ++nt) {
+      float2 l2 = unpair(rs[nt].l);
+      const float2 nc = unpair(rs[nt].nc), dn = unpair(rs[nt].down);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int k = 4; k < 32; k <<= 1) {
+        l2.x += __shfl_xor_sync(0xffffffffu, l2.x, k);
+        l2.y += __shfl_xor_sync(0xffffffffu, l2.y, k);
+      }
+      // elements 0, 2 are columns 2g, 2g + 1 of row 2c, elements 1, 3 of row 2c + 1
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int fr = (mt * (D / 8) + 2 * x + n) * 4 + e;
-            v[n][e] = (sm.join[0][fr][lane] + sm.join[1][fr][lane]) + (sm.join[2][fr][lane] + sm.join[3][fr][lane]);
-          }
+      for (int e = 0; e < 2; ++e) {
+        const int lr = 8 * nt + 2 * c4 + e;
+        const float l = e ? l2.y : l2.x, up = __int_as_float((254 << 23) - __float_as_int(e ? dn.y : dn.x));  // 2^E
+        const float c = rs[nt].thr[e] == -INFINITY ? -INFINITY : -(e ? nc.y : nc.x);
+        if (lr >= rows) continue;
+        if (whole) {
+          const OutRow to(a, b, h, row0 + lr);
+          const float f = row_inverse(l);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int lr = 16 * mt + g + 8 * r, col = 16 * x + 4 * c4;
-          const float4 ov = make_float4(v[0][2 * r], v[1][2 * r], v[0][2 * r + 1], v[1][2 * r + 1]);
-          float cc = cmax[0][r], ll = lsum[0][r];
+          for (int x = 0; x < XV; ++x)
+            *reinterpret_cast<uint32_t*>(to.p + 16 * x + 2 * g) =
+                pack_bf16x2(o[nt][x][e] * up * f, o[nt][x][2 + e] * up * f);
+          if (g == 0) store_lse(a, b, h, row0 + lr, c, l);
+        } else {
 #pragma unroll
-          for (int k = 1; k < MT; ++k)
-            if (k == mt) { cc = cmax[k][r]; ll = lsum[k][r]; }
-          if (lr < rows) {
-            if (whole) {
-              store_out(a, b, h, row0 + lr, col, ov, row_inverse(ll));
-              if (x == 0 && c4 == 0) store_lse(a, b, h, row0 + lr, cc, ll);
-            } else {
-              *reinterpret_cast<float4*>(part + lr * D + col) = ov;
-              if (x == 0 && c4 == 0) { part[R * D + lr] = cc; part[R * D + R + lr] = ll; }
-            }
+          for (int x = 0; x < XV; ++x)
+            *reinterpret_cast<float2*>(part + lr * D + 16 * x + 2 * g) =
+                make_float2(o[nt][x][e] * up, o[nt][x][2 + e] * up);
+          if (g == 0) {
+            sm.c[warp][slot][lr] = c;
+            sm.l[warp][slot][lr] = l;
           }
         }
       }
     }
-    __syncthreads();
+    if (!whole && lane == 0 && (slot == 1 || warp == 0)) {
+      Cut& k = sm.cut[slot == 1 ? warp : W];
+      k.start = u.start;
+      k.end = unit_end;
+      k.b = b; k.h = h; k.row0 = row0; k.rows = rows;
+      k.slot = slot;
+    }
     seg = seg_end;
+  }
+
+  // ---- join the parts of the units that the warps' borders cut
+  __syncthreads();
+  constexpr int V4 = D / 4;
+  for (int k = 0; k <= W; ++k) {
+    const Cut& cut = sm.cut[k];
+    if (cut.slot < 0) continue;
+    const int w0 = k == W ? 0 : k;
+    int w1 = w0 + 1;  // parts: (w0, its slot), then slot 0 of the warps up to w1
+    while (w1 < W && st.s + w1 * share < min(cut.end, st.e)) ++w1;
+    const bool whole = cut.start >= st.s && cut.end <= st.e;
+    float* to = part_of<R, D>(a, blockIdx.x, cut.start < st.s ? 0 : 1);
+    for (int i4 = threadIdx.x; i4 < cut.rows * V4; i4 += Sh::kThreads) {
+      const int r = i4 / V4, col = 4 * (i4 % V4);
+      float c = -INFINITY, l = 0.0f;
+      for (int w = w0; w < w1; ++w) c = fmaxf(c, sm.c[w][w == w0 ? cut.slot : 0][r]);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int w = w0; w < w1; ++w) {
+        const int slot = w == w0 ? cut.slot : 0;
+        const float cw = sm.c[w][slot][r], f = cw == -INFINITY ? 0.0f : ex2f(cw - c);
+        const float4 x = *reinterpret_cast<const float4*>(warp_part<R, D>(a, blockIdx.x * W + w, slot) + r * D + col);
+        l += sm.l[w][slot][r] * f;
+        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+      }
+      if (whole) {
+        store_out(a, cut.b, cut.h, cut.row0 + r, col, o, row_inverse(l));
+        if (col == 0) store_lse(a, cut.b, cut.h, cut.row0 + r, c, l);
+      } else {
+        *reinterpret_cast<float4*>(to + r * D + col) = o;
+        if (col == 0) { to[R * D + r] = c; to[R * D + R + r] = l; }
+      }
+    }
   }
 }
 
-template <int D, int MT, int KF, int VF>
+template <int D, int NT, int KF, int VF>
 int launch_mma(const CacheAttnArgs& a, cudaStream_t s) {
-  constexpr int R = 16 * MT;
+  using Sh = Shape<D, NT>;
   const uint64_t rows = (uint64_t)a.c.pages * a.c.H << a.c.page_shift;
   CUtensorMap mk, mv;
-  if (!tc::make_map(&mk, a.c.codes[0], D, rows, 1, D, rows * D, D, kTile) ||
-      !tc::make_map(&mv, a.c.codes[1], D, rows, 1, D, rows * D, D, kTile))
+  if (!tc::make_map(&mk, a.c.codes[0], D, rows, 1, D, rows * D, D, kBox) ||
+      !tc::make_map(&mv, a.c.codes[1], D, rows, 1, D, rows * D, D, kBox))
     return SAGE_ERR_CUDA;
-  auto* fn = cache_attn_mma_kernel<D, MT, KF, VF>;
-  const size_t smem = sizeof(Smem<D, MT>) + 1024;
+  auto* fn = cache_attn_mma_kernel<D, NT, KF, VF>;
+  constexpr size_t smem = sizeof(Smem<D, NT>) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SAGE_ERR_CUDA;
-  fn<<<kMaxCtas, kThreads, smem, s>>>(mk, mv, a);
+  fn<<<kMaxCtas, Sh::kThreads, smem, s>>>(mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -535,26 +600,31 @@ int launch_mma(const CacheAttnArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<kTile, R, D, kWarps, 256>, a, kMaxCtas) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<kTile, 8 * NT, D, Sh::kWarps, 256>, a, kMaxCtas) == cudaSuccess
              ? SAGE_OK
              : SAGE_ERR_CUDA;
 }
 
-template <int D, int MT>
+template <int D, int NT>
 int by_format(const CacheAttnArgs& a, cudaStream_t s) {
   const bool k8 = a.c.format[0] == SAGE_CACHE_INT8, v8 = a.c.format[1] == SAGE_CACHE_INT8;
-  if (k8) return v8 ? launch_mma<D, MT, SAGE_CACHE_INT8, SAGE_CACHE_INT8>(a, s) : launch_mma<D, MT, SAGE_CACHE_INT8, SAGE_CACHE_E4M3>(a, s);
-  return v8 ? launch_mma<D, MT, SAGE_CACHE_E4M3, SAGE_CACHE_INT8>(a, s) : launch_mma<D, MT, SAGE_CACHE_E4M3, SAGE_CACHE_E4M3>(a, s);
+  if (k8) return v8 ? launch_mma<D, NT, SAGE_CACHE_INT8, SAGE_CACHE_INT8>(a, s) : launch_mma<D, NT, SAGE_CACHE_INT8, SAGE_CACHE_E4M3>(a, s);
+  return v8 ? launch_mma<D, NT, SAGE_CACHE_E4M3, SAGE_CACHE_INT8>(a, s) : launch_mma<D, NT, SAGE_CACHE_E4M3, SAGE_CACHE_E4M3>(a, s);
+}
+
+template <int D>
+int by_rows(const CacheAttnArgs& a, cudaStream_t s) {
+  const int rows = a.T * a.G;
+  return rows <= 8 ? by_format<D, 1>(a, s) : by_format<D, 2>(a, s);
 }
 
 }  // namespace
 
-size_t cache_attn_workspace_bytes() { return (size_t)2 * kMaxCtas * (32 * 128 + 2 * 32) * sizeof(float); }
+// The joined parts of the CTAs (of the widest row tile), then those of their warps.
+size_t cache_attn_workspace_bytes() { return kCtaPartBytes + (size_t)2 * kMaxCtas * 8 * 16 * 128 * sizeof(float); }
 
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
-  const bool one = a.T * a.G <= 16;
-  if (a.c.D == 128) return one ? by_format<128, 1>(a, s) : by_format<128, 2>(a, s);
-  return one ? by_format<64, 1>(a, s) : by_format<64, 2>(a, s);
+  return a.c.D == 128 ? by_rows<128>(a, s) : by_rows<64>(a, s);
 }
 
 }  // namespace sage

@@ -134,7 +134,16 @@ __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta,
   return t;
 }
 
-// Parts in the workspace: [2 * CTA + slot] of R x D sums, R offsets, R denominators.
+constexpr int kMaxCtas = 148;  // one per SM
+constexpr int kMaxRows = 128;  // of a unit
+constexpr size_t kCtaPartBytes = (size_t)2 * kMaxCtas * (kMaxRows * 128 + 2 * kMaxRows) * sizeof(float);
+
+// Parts of the CTAs: [2 * CTA + slot] of R x D sums, R offsets, R denominators;
+// behind them, where warps leave parts too, [2 * warp of the grid + slot] of R x D sums.
+template <int R, int D>
+__device__ __forceinline__ float* warp_part(const CacheAttnArgs& a, int warp, int slot) {
+  return static_cast<float*>(a.workspace) + kCtaPartBytes / sizeof(float) + (size_t)(2 * warp + slot) * (R * D);
+}
 template <int R, int D>
 __device__ __forceinline__ float* part_of(const CacheAttnArgs& a, int cta, int slot) {
   return static_cast<float*>(a.workspace) + (size_t)(2 * cta + slot) * (R * D + 2 * R);
@@ -152,11 +161,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Four columns of a finished row.
+// A finished row of the output, and four columns of one.
+struct OutRow {
+  uint16_t* p;
+  __device__ __forceinline__ OutRow(const CacheAttnArgs& a, int b, int h, int row)
+      : p(a.out + b * a.ob + (row / a.G) * a.on + (h * a.G + row % a.G) * a.oh) {}
+};
 __device__ __forceinline__ void store_out(const CacheAttnArgs& a, int b, int h, int row, int col, float4 o, float inv) {
-  const int t = row / a.G, hq = h * a.G + row % a.G;
-  *reinterpret_cast<uint2*>(a.out + b * a.ob + t * a.on + hq * a.oh + col) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  const OutRow to(a, b, h, row);
+  *reinterpret_cast<uint2*>(to.p + col) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 // 1 / l and the row's lse; a row that saw nothing has l = 0.
 __device__ __forceinline__ float row_inverse(float l) { return l == 0.0f ? 0.0f : __frcp_rn(l); }
