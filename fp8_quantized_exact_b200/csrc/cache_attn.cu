@@ -25,7 +25,7 @@
 // stretch per warp, and the warps run alone: lane 0 keeps its ring of K and V
 // tiles of 32 keys filled by TMA, ahead and across units; a unit that lies
 // within the warp's stretch is finished from its registers, one that is cut
-// leaves a part in the workspace, and the CTA joins its warps' parts once, at its
+// leaves a part in shared memory, and the CTA joins its warps' parts once, at its
 // end.  A tile is two boxes of 16 keys, the smallest page, so a box never crosses
 // one.
 #include "cache_attn.cuh"
@@ -129,19 +129,23 @@ __device__ __forceinline__ uint32_t swizzled(int key, int chunk) {
   return key * D + ((D == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3)) << 4);
 }
 
-// Launch shape by the number of 8-row groups.
+// Launch shape by the number of 8-row groups.  The registers leave room for a
+// block of the joining kernel beside the CTA.
 template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kWarps = NT == 1 ? 10 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = (D == 128 ? 1 : 2) * (kWarps == 12 ? 2 : 3);
+  static constexpr int kRegs = NT == 1 ? 168 : 224;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static_assert(kStages * kTile * D >= 8 * NT * D * 4, "a part fits a warp's ring of K");
 };
 
 // The last unit of a warp's stretch, and the first of the CTA's: what the CTA's
 // join needs of it.  slot -1: the warp left no such part.
 struct Cut {
-  long long start, end;  // of the unit, in the list
+  unsigned start, end;  // of the unit, in the list
   int slot, b, h, row0, rows;
+  const float* sums;
 };
 
 template <int D, int NT>
@@ -149,10 +153,11 @@ struct Smem {
   using Sh = Shape<D, NT>;
   alignas(1024) uint8_t k[Sh::kWarps][Sh::kStages][kTile * D];
   alignas(1024) uint8_t v[Sh::kWarps][Sh::kStages][kTile * D];
+  float head[Sh::kWarps][8 * NT * D];  // sums of slot 0, where the stretch goes on behind them; the others lie in the ring of K
   float c[Sh::kWarps][2][8 * NT], l[Sh::kWarps][2][8 * NT];  // of the parts
   Cut cut[Sh::kWarps + 1];  // [w]: a unit that begins in warp w's stretch and goes on; [kWarps]: one that began before the CTA's
+  const float* at0[Sh::kWarps];  // sums of slot 0
   uint64_t full[Sh::kWarps][Sh::kStages];
-  StretchSmem stretch;
 };
 
 // Running state of the thread's rows 8 nt + 2c and 8 nt + 2c + 1.
@@ -162,7 +167,7 @@ struct Rows {
 };
 
 template <int D, int NT, int KF, int VF>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
+__global__ void __maxnreg__((Shape<D, NT>::kRegs))
     cache_attn_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const CacheAttnArgs a) {
   using Sh = Shape<D, NT>;
@@ -171,10 +176,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
 
-  if (threadIdx.x <= W) sm.cut[threadIdx.x].slot = -1;
-  if (threadIdx.x < W * S) tc::mbar_init(&sm.full[0][0] + threadIdx.x, 1);
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Stretch st = find_stretch<kTile, R, W>(a, blockIdx.x, gridDim.x);
   if (blockIdx.x == 0)  // lengths that cannot be
     for (int b = threadIdx.x; b < a.B; b += Sh::kThreads) {
       const int ctx = a.context[b], cnt = a.count ? a.count[b] : a.T;
@@ -182,22 +185,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
           (long long)ctx + cnt > ((long long)a.c.table_pages << a.c.page_shift))
         flag_bad(a.c.status, kWhereAttn);
     }
-  const Stretch st = find_stretch<kTile, R, Sh::kThreads, W>(a, blockIdx.x, gridDim.x, sm.stretch);
-  __syncthreads();
   if (st.s >= st.e) return;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) tc::mbar_init(&sm.full[warp][s], 1);
+    sm.cut[warp].slot = -1;
+    if (warp == 0) sm.cut[W].slot = -1;
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
 
   // ---- this warp's tiles: list indices [first, last)
-  const long long share = st.share / W, first = min(st.s + warp * share, st.e), last = min(first + share, st.e);
+  const unsigned share = st.share / W, first = min(st.s + warp * share, st.e), last = min(first + share, st.e);
   const int n_tiles = (int)(last - first);
+  const Place begin = n_tiles > 0 ? place_of<kTile, R>(a, first) : Place{};
   // cache rows of the two boxes of tiles 32 blk + lane, -1 for a box without keys: this block of 32 tiles and the next
-  Place walk = st.p;
+  Place walk = begin;
   auto rows_of_block = [&](int blk, int& r0, int& r1) {
     r0 = r1 = -1;
-    const long long idx = first + 32 * blk + lane;
+    const unsigned idx = first + 32 * blk + lane;
     if (idx >= last) return;
     go_to<kTile, R>(a, walk, idx);
     const Unit u = unit_of(walk, idx);
-    const int64_t slot = (idx - u.start) * kTile, end = (int64_t)walk.s.ctx + walk.s.cnt;
+    const int64_t slot = (int64_t)(idx - u.start) * kTile, end = (int64_t)walk.s.ctx + walk.s.cnt;
     r0 = (int)cache_row(a.c, walk.b, u.h, slot);
     if (r0 < 0) flag_bad(a.c.status, kWhereAttn);
     if (slot + kBox < end) {
@@ -205,8 +214,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       if (r1 < 0) flag_bad(a.c.status, kWhereAttn);
     }
   };
-  int block = 0, ra0, ra1, rb0 = -1, rb1 = -1;
-  rows_of_block(0, ra0, ra1);
+  int block = 0, ra0 = -1, ra1 = -1, rb0 = -1, rb1 = -1;
+  if (n_tiles > 0) rows_of_block(0, ra0, ra1);
   if (n_tiles > 32) rows_of_block(1, rb0, rb1);
   auto row0_of = [&](int i) { return __shfl_sync(0xffffffffu, (i >> 5) == block ? ra0 : rb0, i & 31); };
   auto row1_of = [&](int i) { return __shfl_sync(0xffffffffu, (i >> 5) == block ? ra1 : rb1, i & 31); };
@@ -244,14 +253,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   const uint32_t ksw = swizzled<D>(key_of(g), c4);
   const int vkey = 8 * ((lane >> 3) & 1) + key_of(lane & 7), vchunk = lane >> 4;
 
-  Place at = st.p;
+  Place at = begin;
   int i = 0;
-  for (long long seg = first; seg < last;) {
+  for (unsigned seg = first; seg < last;) {
     go_to<kTile, R>(a, at, seg);
     const Unit u = unit_of(at, seg);
     const int b = at.b, h = u.h, row0 = u.rt * R;
     const int ctx = at.s.ctx, cnt = at.s.cnt, rows = min(R, cnt * a.G - row0);
-    const long long unit_end = u.start + at.s.n, seg_end = min(unit_end, last);
+    const unsigned unit_end = u.start + at.s.n, seg_end = min(unit_end, last);
     const int i_end = (int)(seg_end - first);
 
     // ---- Q rows as B fragments: of k step 4x + y, k = 2c, 2c+1 and 2c+8, 2c+9 are channels 64x + 16c + 4y + 0, 2
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         phase ^= 1u << s;
         dead = __any_sync(0xffffffffu, dead);
         if (!dead) {
-          const int64_t slot0 = (first + i - u.start) * kTile;
+          const int64_t slot0 = (int64_t)(first + i - u.start) * kTile;
           const uint32_t ka = kbase + s * kTile * D, va = vbase + s * kTile * D;
           if (slot0 + kTile <= ctx && r0 >= 0 && r1 >= 0) tile(std::false_type{}, ka, va, ks, vs, slot0, true, true);
           else tile(std::true_type{}, ka, va, ks, vs, slot0, r0 >= 0, r1 >= 0);
@@ -494,7 +503,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     // ---- the unit's rows, or this warp's part of them
     const bool whole = seg == u.start && seg_end == unit_end;
     const int slot = seg == u.start ? 1 : 0;
-    float* part = warp_part<R, D>(a, blockIdx.x * W + warp, slot);
+    // a warp's last part lies in its ring, which is used up
+    float* part = seg_end == last ? reinterpret_cast<float*>(sm.k[warp][0]) : sm.head[warp];
+    if (!whole) __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float2 l2 = unpair(rs[nt].l);
@@ -537,41 +548,39 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       k.end = unit_end;
       k.b = b; k.h = h; k.row0 = row0; k.rows = rows;
       k.slot = slot;
+      k.sums = part;
     }
+    if (!whole && lane == 0 && slot == 0) sm.at0[warp] = part;
     seg = seg_end;
   }
 
   // ---- join the parts of the units that the warps' borders cut
   __syncthreads();
   constexpr int V4 = D / 4;
-  for (int k = 0; k <= W; ++k) {
-    const Cut& cut = sm.cut[k];
-    if (cut.slot < 0) continue;
-    const int w0 = k == W ? 0 : k;
+  for (int item = threadIdx.x / V4; item < (W + 1) * R; item += Sh::kThreads / V4) {
+    const int r = item % R, col = 4 * (threadIdx.x % V4);
+    const Cut& cut = sm.cut[item / R];
+    if (cut.slot < 0 || r >= cut.rows) continue;
+    const int w0 = item / R == W ? 0 : item / R;
     int w1 = w0 + 1;  // parts: (w0, its slot), then slot 0 of the warps up to w1
     while (w1 < W && st.s + w1 * share < min(cut.end, st.e)) ++w1;
-    const bool whole = cut.start >= st.s && cut.end <= st.e;
-    float* to = part_of<R, D>(a, blockIdx.x, cut.start < st.s ? 0 : 1);
-    for (int i4 = threadIdx.x; i4 < cut.rows * V4; i4 += Sh::kThreads) {
-      const int r = i4 / V4, col = 4 * (i4 % V4);
-      float c = -INFINITY, l = 0.0f;
-      for (int w = w0; w < w1; ++w) c = fmaxf(c, sm.c[w][w == w0 ? cut.slot : 0][r]);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int w = w0; w < w1; ++w) {
-        const int slot = w == w0 ? cut.slot : 0;
-        const float cw = sm.c[w][slot][r], f = cw == -INFINITY ? 0.0f : ex2f(cw - c);
-        const float4 x = *reinterpret_cast<const float4*>(warp_part<R, D>(a, blockIdx.x * W + w, slot) + r * D + col);
-        l += sm.l[w][slot][r] * f;
-        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
-      }
-      if (whole) {
-        store_out(a, cut.b, cut.h, cut.row0 + r, col, o, row_inverse(l));
-        if (col == 0) store_lse(a, cut.b, cut.h, cut.row0 + r, c, l);
-      } else {
-        *reinterpret_cast<float4*>(to + r * D + col) = o;
-        if (col == 0) { to[R * D + r] = c; to[R * D + R + r] = l; }
-      }
+    float c = sm.c[w0][cut.slot][r], l = 0.0f;
+    for (int w = w0 + 1; w < w1; ++w) c = fmaxf(c, sm.c[w][0][r]);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int w = w0; w < w1; ++w) {
+      const int slot = w == w0 ? cut.slot : 0;
+      const float cw = sm.c[w][slot][r], f = cw == -INFINITY ? 0.0f : ex2f(cw - c);
+      const float4 x = *reinterpret_cast<const float4*>((w == w0 ? cut.sums : sm.at0[w]) + r * D + col);
+      l += sm.l[w][slot][r] * f;
+      o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+    }
+    if (cut.start >= st.s && cut.end <= st.e) {
+      store_out(a, cut.b, cut.h, cut.row0 + r, col, o, row_inverse(l));
+      if (col == 0) store_lse(a, cut.b, cut.h, cut.row0 + r, c, l);
+    } else {
+      float* to = part_of<R, D>(a, blockIdx.x, cut.start < st.s ? 0 : 1);
+      *reinterpret_cast<float4*>(to + r * D + col) = o;
+      if (col == 0) { to[R * D + r] = c; to[R * D + R + r] = l; }
     }
   }
 }
@@ -579,6 +588,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 template <int D, int NT, int KF, int VF>
 int launch_mma(const CacheAttnArgs& a, cudaStream_t s) {
   using Sh = Shape<D, NT>;
+  if (!list_fits<kTile, 8 * NT>(a)) return SAGE_ERR_UNSUPPORTED;
   const uint64_t rows = (uint64_t)a.c.pages * a.c.H << a.c.page_shift;
   CUtensorMap mk, mv;
   if (!tc::make_map(&mk, a.c.codes[0], D, rows, 1, D, rows * D, D, kBox) ||
@@ -591,18 +601,7 @@ int launch_mma(const CacheAttnArgs& a, cudaStream_t s) {
     return SAGE_ERR_CUDA;
   fn<<<kMaxCtas, Sh::kThreads, smem, s>>>(mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kMaxCtas, 2);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<kTile, 8 * NT, D, Sh::kWarps, 256>, a, kMaxCtas) == cudaSuccess
-             ? SAGE_OK
-             : SAGE_ERR_CUDA;
+  return launch_join<kTile, 8 * NT, D, Sh::kWarps>(a, s);
 }
 
 template <int D, int NT>
@@ -620,8 +619,7 @@ int by_rows(const CacheAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The joined parts of the CTAs (of the widest row tile), then those of their warps.
-size_t cache_attn_workspace_bytes() { return kCtaPartBytes + (size_t)2 * kMaxCtas * 8 * 16 * 128 * sizeof(float); }
+size_t cache_attn_workspace_bytes() { return kPartBytes; }
 
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   return a.c.D == 128 ? by_rows<128>(a, s) : by_rows<64>(a, s);

@@ -17,10 +17,10 @@ namespace sage {
 namespace cattn {
 
 struct Seq {
-  int ctx, cnt;     // context and drafted tokens
-  int n;            // tiles
-  int rt;           // row tiles
-  long long per;    // tiles of all its units
+  int ctx, cnt;      // context and drafted tokens
+  unsigned n;        // tiles of a unit
+  unsigned rt;       // row tiles
+  unsigned per;      // tiles of all its units (the launch checks that the list stays below 2^31)
 };
 
 template <int TILE, int R>
@@ -28,22 +28,22 @@ __device__ __forceinline__ Seq seq_of(const CacheAttnArgs& a, int b) {
   Seq s;
   s.ctx = max(__ldg(a.context + b), 0);
   s.cnt = a.count ? min(max(__ldg(a.count + b), 0), a.T) : a.T;
-  const long long cap = (long long)a.c.table_pages << a.c.page_shift;
-  s.n = (int)((min((long long)s.ctx + s.cnt, cap) + TILE - 1) / TILE);
+  const unsigned cap = (unsigned)a.c.table_pages << a.c.page_shift;
+  s.n = (min((unsigned)s.ctx + (unsigned)s.cnt, cap) + TILE - 1) / TILE;
   s.rt = (s.cnt * a.G + R - 1) / R;
-  s.per = (long long)a.c.H * s.rt * s.n;
+  s.per = a.c.H * s.rt * s.n;
   return s;
 }
 
 // A place in the list: the sequence b whose tiles begin at `base`.
 struct Place {
-  long long base;
+  unsigned base;
   int b;
   Seq s;
 };
 // Moves on to the sequence of tile idx (idx >= base, below the list's end).
 template <int TILE, int R>
-__device__ __forceinline__ void go_to(const CacheAttnArgs& a, Place& p, long long idx) {
+__device__ __forceinline__ void go_to(const CacheAttnArgs& a, Place& p, unsigned idx) {
   while (idx >= p.base + p.s.per) {
     p.base += p.s.per;
     ++p.b;
@@ -51,99 +51,83 @@ __device__ __forceinline__ void go_to(const CacheAttnArgs& a, Place& p, long lon
   }
 }
 struct Unit {
-  int h, rt;         // head of the cache, row tile
-  long long start;   // list index of its first tile
+  int h, rt;       // head of the cache, row tile
+  unsigned start;  // list index of its first tile
 };
-__device__ __forceinline__ Unit unit_of(const Place& p, long long idx) {
-  const unsigned long long u = (unsigned long long)(idx - p.base) / (unsigned)p.s.n;
+__device__ __forceinline__ Unit unit_of(const Place& p, unsigned idx) {
+  const unsigned u = (idx - p.base) / p.s.n;
   Unit r;
-  r.rt = (int)(u % (unsigned)p.s.rt);
-  r.h = (int)(u / (unsigned)p.s.rt);
-  r.start = p.base + (long long)u * p.s.n;
+  r.rt = (int)(u % p.s.rt);
+  r.h = (int)(u / p.s.rt);
+  r.start = p.base + u * p.s.n;
   return r;
 }
 
-// The stretch [s, e) of CTA `cta` of at most `ctas`, by a whole block (THREADS
-// threads): lengths are summed and searched THREADS sequences at a time.
-// STEP: stretches are multiples of it (what a CTA does at once).
+// The stretch [s, e) of CTA `cta` of `ctas`, and the place of a tile in it.
+// Every warp finds it for itself, 32 sequences at a time, which needs no
+// barrier.  STEP: stretches are multiples of it.
 struct Stretch {
-  long long s, e, share, total;
+  unsigned s, e, share, total;
+};
+template <int TILE, int R, int STEP>
+__device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  unsigned sum = 0;
+  for (int b = lane; b < a.B; b += 32) sum += seq_of<TILE, R>(a, b).per;
+  Stretch t;
+  t.total = __reduce_add_sync(0xffffffffu, sum);
+  t.share = max((t.total + ctas * STEP - 1) / (ctas * STEP), 1u) * STEP;
+  t.s = min((unsigned)cta * t.share, t.total);
+  t.e = min(t.s + t.share, t.total);
+  return t;
+}
+template <int TILE, int R>
+__device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned idx) {
+  const int lane = threadIdx.x & 31;
   Place p;
-};
-struct StretchSmem {
-  long long warp_sum[32];
-  long long base;
-  int b;
-};
-template <int TILE, int R, int THREADS, int STEP>
-__device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta, int ctas, StretchSmem& sm) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // inclusive sum over the block of one value per thread, and the total
-  auto block_scan = [&](long long v, long long& total) {
+  p.base = 0;
+  p.b = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    Seq s;
+    s.ctx = s.cnt = 0;
+    s.n = s.rt = 1;
+    s.per = 0;
+    if (b0 + lane < a.B) s = seq_of<TILE, R>(a, b0 + lane);
+    unsigned incl = s.per;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
+      const unsigned w = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += w;
     }
-    __syncthreads();
-    if (lane == 31) sm.warp_sum[warp] = v;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += sm.warp_sum[w];
-      total += sm.warp_sum[w];
+    const unsigned here = __ballot_sync(0xffffffffu, idx < p.base + incl);
+    if (here) {  // the first lane whose sum passes idx
+      const int l = __ffs(here) - 1;
+      p.b = b0 + l;
+      p.base += __shfl_sync(0xffffffffu, incl - s.per, l);
+      p.s.ctx = __shfl_sync(0xffffffffu, s.ctx, l);
+      p.s.cnt = __shfl_sync(0xffffffffu, s.cnt, l);
+      p.s.n = __shfl_sync(0xffffffffu, s.n, l);
+      p.s.rt = __shfl_sync(0xffffffffu, s.rt, l);
+      p.s.per = __shfl_sync(0xffffffffu, s.per, l);
+      return p;
     }
-    return v + before;
-  };
-  auto tiles = [&](int b) { return b < a.B ? seq_of<TILE, R>(a, b).per : 0; };
-  Stretch t;
-  t.total = 0;
-  long long mine = tiles(threadIdx.x), incl = 0, part;
-  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    incl = block_scan(b0 == 0 ? mine : tiles(b0 + threadIdx.x), part);
-    t.total += part;
+    p.base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  t.share = (t.total + ctas - 1) / ctas;
-  t.share = max((t.share + STEP - 1) / STEP, 1ll) * STEP;
-  t.s = min(cta * t.share, t.total);
-  t.e = min(t.s + t.share, t.total);
-  t.p.base = 0;
-  t.p.b = 0;
-  if (t.s < t.e) {
-    long long before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-      if (a.B > THREADS) {  // otherwise the one block of sums is still here
-        mine = tiles(b0 + threadIdx.x);
-        incl = block_scan(mine, part);
-      } else {
-        part = t.total;
-      }
-      if (t.s >= before + incl - mine && t.s < before + incl) {
-        sm.base = before + incl - mine;
-        sm.b = b0 + threadIdx.x;
-      }
-      before += part;
-      if (before > t.s) break;
-    }
-    __syncthreads();
-    t.p.base = sm.base;
-    t.p.b = sm.b;
-    t.p.s = seq_of<TILE, R>(a, t.p.b);
-  }
-  return t;
+  return p;  // not reached for idx below the list's end
+}
+
+// The longest list that the arguments allow has to stay below 2^31 tiles.
+template <int TILE, int R>
+inline bool list_fits(const CacheAttnArgs& a) {
+  const double n = (((double)a.c.table_pages * (1 << a.c.page_shift)) + TILE - 1) / TILE;
+  return n * a.B * a.c.H * ((a.T * a.G + R - 1) / R) < 2147483648.0;
 }
 
 constexpr int kMaxCtas = 148;  // one per SM
 constexpr int kMaxRows = 128;  // of a unit
-constexpr size_t kCtaPartBytes = (size_t)2 * kMaxCtas * (kMaxRows * 128 + 2 * kMaxRows) * sizeof(float);
+constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (kMaxRows * 128 + 2 * kMaxRows) * sizeof(float);
 
-// Parts of the CTAs: [2 * CTA + slot] of R x D sums, R offsets, R denominators;
-// behind them, where warps leave parts too, [2 * warp of the grid + slot] of R x D sums.
-template <int R, int D>
-__device__ __forceinline__ float* warp_part(const CacheAttnArgs& a, int warp, int slot) {
-  return static_cast<float*>(a.workspace) + kCtaPartBytes / sizeof(float) + (size_t)(2 * warp + slot) * (R * D);
-}
+// Parts in the workspace: [2 * CTA + slot] of R x D sums, R offsets, R denominators.
 template <int R, int D>
 __device__ __forceinline__ float* part_of(const CacheAttnArgs& a, int cta, int slot) {
   return static_cast<float*>(a.workspace) + (size_t)(2 * cta + slot) * (R * D + 2 * R);
@@ -180,48 +164,89 @@ __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, int b, int h, 
 }
 
 // Joins the parts of the unit that begins in CTA blockIdx.x's stretch and is
-// cut by its end; blockIdx.y of gridDim.y takes a share of the columns.
-template <int TILE, int R, int D, int STEP, int THREADS>
-__global__ void __launch_bounds__(THREADS) cache_attn_join_kernel(const CacheAttnArgs a, int ctas) {
-  __shared__ StretchSmem sm;
-  __shared__ float c_row[R], l_row[R];
-  const Stretch st = find_stretch<TILE, R, THREADS, STEP>(a, blockIdx.x, ctas, sm);
+// cut by its end; blockIdx.y of gridDim.y takes a share of the rows.  The
+// blocks become resident beside the CTAs of the main kernel, find their unit
+// and wait for them.
+constexpr int kJoinThreads = 128;
+template <int TILE, int R, int D, int STEP>
+__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const CacheAttnArgs a, int ctas) {
+  constexpr int RB = 8;  // rows at a time
+  __shared__ float c_s[RB][kMaxCtas], l_s[RB][kMaxCtas];  // offsets, then weights; denominators
+  __shared__ float c_row[RB], l_row[RB];
+  const Stretch st = find_stretch<TILE, R, STEP>(a, blockIdx.x, ctas);
+  Place p;
+  Unit u;
+  unsigned end = 0;
+  if (st.s < st.e) {
+    p = place_of<TILE, R>(a, st.e - 1);
+    u = unit_of(p, st.e - 1);
+    end = u.start + p.s.n;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // from here on the parts are written
-  if (st.s >= st.e) return;
-  Place p = st.p;
-  go_to<TILE, R>(a, p, st.e - 1);
-  const Unit u = unit_of(p, st.e - 1);
-  const long long end = u.start + p.s.n;
-  if (u.start < st.s || end <= st.e) return;
-  const int last = (int)((end - 1) / st.share);
+  if (st.s >= st.e || u.start < st.s || end <= st.e) return;
+  const int first = blockIdx.x, np = (int)((end - 1) / st.share) - first + 1;
   const int rows = min(R, p.s.cnt * a.G - u.rt * R);
-  auto part = [&](int i) { return part_of<R, D>(a, i, i == (int)blockIdx.x ? 1 : 0); };
-  for (int r = threadIdx.x; r < rows; r += THREADS) {
-    float c = -INFINITY, l = 0.0f;
-    for (int i = blockIdx.x; i <= last; ++i) c = fmaxf(c, part(i)[R * D + r]);
-    for (int i = blockIdx.x; i <= last; ++i) {
-      const float ci = part(i)[R * D + r];
-      l += part(i)[R * D + R + r] * (ci == -INFINITY ? 0.0f : ex2f(ci - c));
+  auto part = [&](int i) { return part_of<R, D>(a, first + i, i == 0 ? 1 : 0); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r0 = blockIdx.y * RB; r0 < rows; r0 += gridDim.y * RB) {
+    const int nr = min(RB, rows - r0);
+    for (int i = threadIdx.x; i < np * RB; i += kJoinThreads) {
+      const int k = i / RB, r = i % RB;
+      if (r < nr) {
+        c_s[r][k] = part(k)[R * D + r0 + r];
+        l_s[r][k] = part(k)[R * D + R + r0 + r];
+      }
     }
-    c_row[r] = c;
-    l_row[r] = l;
-    if (blockIdx.y == 0) store_lse(a, p.b, u.h, u.rt * R + r, c, l);
-  }
-  __syncthreads();
-  constexpr int V4 = D / 4;
-  for (int i4 = blockIdx.y * THREADS + threadIdx.x; i4 < rows * V4; i4 += gridDim.y * THREADS) {
-    const int r = i4 / V4, col = 4 * (i4 % V4);
-    const float c = c_row[r];
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = blockIdx.x; i <= last; ++i) {
-      const float ci = part(i)[R * D + r];
-      const float f = ci == -INFINITY ? 0.0f : ex2f(ci - c);
-      const float4 x = *reinterpret_cast<const float4*>(part(i) + r * D + col);
-      o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+    __syncthreads();
+    for (int r = warp; r < nr; r += kJoinThreads / 32) {
+      float c = -INFINITY, l = 0.0f;
+      for (int k = lane; k < np; k += 32) c = fmaxf(c, c_s[r][k]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+      for (int k = lane; k < np; k += 32) {
+        const float f = c_s[r][k] == -INFINITY ? 0.0f : ex2f(c_s[r][k] - c);
+        l += l_s[r][k] * f;
+        c_s[r][k] = f;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        c_row[r] = c;
+        l_row[r] = l;
+      }
     }
-    store_out(a, p.b, u.h, u.rt * R + r, col, o, row_inverse(l_row[r]));
+    __syncthreads();
+    constexpr int V4 = D / 4;
+    for (int i4 = threadIdx.x; i4 < nr * V4; i4 += kJoinThreads) {
+      const int r = i4 / V4, col = 4 * (i4 % V4);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int k = 0; k < np; ++k) {
+        const float f = c_s[r][k];
+        const float4 x = *reinterpret_cast<const float4*>(part(k) + (r0 + r) * D + col);
+        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+      }
+      store_out(a, p.b, u.h, u.rt * R + r0 + r, col, o, row_inverse(l_row[r]));
+      if (col == 0) store_lse(a, p.b, u.h, u.rt * R + r0 + r, c_row[r], l_row[r]);
+    }
+    __syncthreads();
   }
+}
+
+// Behind the main kernel on its stream, as its programmatic dependent.
+template <int TILE, int R, int D, int STEP>
+int launch_join(const CacheAttnArgs& a, cudaStream_t s) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxCtas, R >= 64 ? 4 : 1);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<TILE, R, D, STEP>, a, kMaxCtas) == cudaSuccess ? SAGE_OK
+                                                                                                       : SAGE_ERR_CUDA;
 }
 
 }  // namespace cattn
