@@ -370,186 +370,7 @@ def sage_debug_qk_s32(q_i8, q_scale, k_i8, k_scale, v_fp8, v_scale, B, N, H, D, 
            "sage_debug_qk_s32")
 
 
-# ------------------------------------------- rotary positions and the cache
-def _on_device(what, *tensors):
-    """The CUDA device that the tensors share; it has to be the current one,
-    on which the library launches."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{what}: tensors must be on the current CUDA device {dev}, got one on {t.device}")
-
-
-def _vector(t, n, what, name):
-    """Device address of a contiguous int32 [n] tensor, or None."""
-    import torch
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: {name} must be a contiguous CUDA int32 [{n}] tensor")
-    return t.data_ptr()
-
-
-def _formats():
-    import torch
-    return {torch.int8: SAGE_CACHE_INT8, torch.float8_e4m3fn: SAGE_CACHE_E4M3}
-
-
-def _cache(cache, what) -> sage_cache:
-    """The C struct of a cache (k, k_scale, v, v_scale): codes int8 or
-    float8_e4m3fn [pages, H, page_size, D], scales float32 [pages, H, page_size]."""
-    import torch
-    k, ks, v, vs = cache
-    fmt = _formats()
-    if (k.dim() != 4 or k.shape != v.shape or k.dtype not in fmt or v.dtype not in fmt or ks.shape != k.shape[:3] or
-            vs.shape != ks.shape or ks.dtype != torch.float32 or vs.dtype != torch.float32 or not k.is_cuda or
-            not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous())):
-        raise ValueError(f"{what}: the cache must be four contiguous CUDA tensors, codes int8 or float8_e4m3fn "
-                         "[pages, H, page_size, D] and scales float32 [pages, H, page_size]")
-    pages, H, page, D = k.shape
-    return sage_cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), fmt[k.dtype], fmt[v.dtype], pages,
-                      page, H, D)
-
-
-def _table(page_table, B, what):
-    import torch
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B or
-            not page_table.is_contiguous() or not page_table.is_cuda):
-        raise ValueError(f"{what}: page_table must be a contiguous CUDA int32 [{B}, pages of a sequence] tensor")
-    return page_table.data_ptr(), page_table.shape[1]
-
-
-def _out_strides(t, shape, what):
-    import torch
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.stride(3) != 1 or not t.is_cuda:
-        raise ValueError(f"{what}: outputs must be CUDA bfloat16 {tuple(shape)} with unit stride over D")
-    return t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)
-
-
-def sage_rope_freqs(rot_dim, base=10000.0, scaling=SAGE_ROPE_PLAIN, factor=1.0, trained_len=4096.0, beta_fast=32.0,
-                    beta_slow=1.0, device="cuda"):
-    """(inv_freq, mscale) for sage_rope: FP64 [rot_dim/2] on `device`, and a float."""
-    import torch
-    out = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
-    mscale = ctypes.c_float(1.0)
-    cfg = sage_rope_config(int(scaling), int(rot_dim), float(base), float(factor), float(trained_len),
-                           float(beta_fast), float(beta_slow))
-    _check(lib().sage_rope_freqs(ctypes.byref(cfg), out.data_ptr(), ctypes.byref(mscale)), "sage_rope_freqs")
-    return out.to(device), mscale.value
-
-
-def sage_rope(q, k, q_out, k_out, positions, inv_freq, mscale=1.0, layout=SAGE_ROPE_HALF, rot_dim=None, inverse=False,
-              stream=None):
-    """Rotary positions on q and k (k and k_out may be None).  positions:
-    int32 [B, N], [N] (shared by the batch) or None (0 .. N-1); rot_dim None:
-    2 * len(inv_freq)."""
-    import torch
-    B, N, Hq, D = q.shape
-    rot_dim = 2 * inv_freq.shape[0] if rot_dim is None else int(rot_dim)
-    if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or not inv_freq.is_contiguous() or \
-            2 * inv_freq.numel() != rot_dim:
-        raise ValueError("sage_rope: inv_freq must be a contiguous CUDA float64 [rot_dim / 2] tensor")
-    pos, pos_stride = None, 0
-    if positions is not None:
-        if positions.dtype != torch.int32 or not positions.is_cuda or positions.stride(-1) != 1 or \
-                tuple(positions.shape) not in ((N,), (B, N)):
-            raise ValueError("sage_rope: positions must be a CUDA int32 [B, N] or [N] tensor with unit stride over N")
-        pos, pos_stride = positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0
-    vq, oq = _view(q), _out_strides(q_out, q.shape, "sage_rope")
-    if k is None:
-        vk, ok, Hk = sage_view_bf16(None, 0, 0, 0), (None, 0, 0, 0), 0
-    else:
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != D:
-            raise ValueError("sage_rope: q and k must agree in B, N and D")
-        vk, ok, Hk = _view(k), _out_strides(k_out, k.shape, "sage_rope"), k.shape[2]
-    _on_device("sage_rope", q, k, q_out, k_out, positions, inv_freq)
-    _check(lib().sage_rope(vq, Hq, *oq, vk, Hk, *ok, pos, pos_stride, inv_freq.data_ptr(), float(mscale), int(layout),
-                           rot_dim, 1 if inverse else 0, B, N, D, _stream(stream)), "sage_rope")
-
-
-def sage_cache_append(cache, k, v, page_table, start, count, workspace, stream=None):
-    """Quantise the first count[b] tokens of k and v [B, N, H, D] into the
-    slots from start[b] on (start, count: int32 [B]; None: 0 and N).  cache:
-    (k, k_scale, v, v_scale), see cache_buffers."""
-    c = _cache(cache, "sage_cache_append")
-    B, N, H, D = k.shape
-    if v.shape != k.shape or H != c.H or D != c.D:
-        raise ValueError("sage_cache_append: k and v must be [B, N, H, D] with the cache's H and D")
-    table, per = _table(page_table, B, "sage_cache_append")
-    first, n = _vector(start, B, "sage_cache_append", "start"), _vector(count, B, "sage_cache_append", "count")
-    vk, vv = _view(k), _view(v)
-    _on_device("sage_cache_append", *cache, k, v, page_table, start, count, workspace)
-    _check(lib().sage_cache_append(ctypes.addressof(c), vk, vv, table, per, first, n, B, N, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)),
-           "sage_cache_append")
-
-
-def sage_cache_read(cache, page_table, start, count, k_out, v_out, workspace, stream=None):
-    """Slots start[b] .. start[b] + count[b] - 1 of each sequence as BF16 into
-    the first rows of k_out and v_out [B, N, H, D] (either may be None); the
-    other rows are left as they were."""
-    c = _cache(cache, "sage_cache_read")
-    like = k_out if k_out is not None else v_out
-    if like is None:
-        raise ValueError("sage_cache_read: neither k_out nor v_out")
-    B, N = like.shape[:2]
-    shape = (B, N, c.H, c.D)
-    table, per = _table(page_table, B, "sage_cache_read")
-    first, n = _vector(start, B, "sage_cache_read", "start"), _vector(count, B, "sage_cache_read", "count")
-    ok = (None, 0, 0, 0) if k_out is None else _out_strides(k_out, shape, "sage_cache_read")
-    ov = (None, 0, 0, 0) if v_out is None else _out_strides(v_out, shape, "sage_cache_read")
-    _on_device("sage_cache_read", *cache, page_table, start, count, k_out, v_out, workspace)
-    _check(lib().sage_cache_read(ctypes.addressof(c), table, per, first, n, *ok, *ov, B, N, workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)),
-           "sage_cache_read")
-
-
-def sage_cache_attn(q, cache, page_table, context, count, mask, out, lse, sm_scale, workspace, stream=None):
-    """Attention of the T new or drafted tokens of each sequence, q [B, T, Hq,
-    D], over its context[b] cached tokens and, by mask (int32 [B, T,
-    ceil(T/32)]; None: j <= i), the drafted ones in the slots behind them.
-    count: int32 [B] or None (T); lse: float32 [B, T, Hq] or None."""
-    import torch
-    c = _cache(cache, "sage_cache_attn")
-    B, T, Hq, D = q.shape
-    if D != c.D or c.H == 0 or Hq % c.H:
-        raise ValueError("sage_cache_attn: q must be [B, T, Hq, D] with the cache's D and a multiple of its heads")
-    table, per = _table(page_table, B, "sage_cache_attn")
-    if context is None:
-        raise ValueError("sage_cache_attn: context is missing")
-    ctx, n = _vector(context, B, "sage_cache_attn", "context"), _vector(count, B, "sage_cache_attn", "count")
-    if mask is not None and (mask.dtype != torch.int32 or tuple(mask.shape) != (B, T, -(-T // 32)) or
-                             not mask.is_contiguous() or not mask.is_cuda):
-        raise ValueError(f"sage_cache_attn: mask must be a contiguous CUDA int32 {(B, T, -(-T // 32))} tensor")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, T, Hq) or
-                            not lse.is_contiguous() or not lse.is_cuda):
-        raise ValueError(f"sage_cache_attn: lse must be a contiguous CUDA float32 {(B, T, Hq)} tensor")
-    vq, o = _view(q), _out_strides(out, q.shape, "sage_cache_attn")
-    _on_device("sage_cache_attn", q, *cache, page_table, context, count, mask, out, lse, workspace)
-    _check(lib().sage_cache_attn(vq, ctypes.addressof(c), table, per, ctx, n, None if mask is None else mask.data_ptr(),
-                                 *o, None if lse is None else lse.data_ptr(), B, T, Hq, float(sm_scale),
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 _stream(stream)),
-           "sage_cache_attn")
-
-
-def sage_clear_device_status(workspace, stream=None):
-    _check(lib().sage_clear_device_status(_ptr(workspace), _stream(stream)), "sage_clear_device_status")
-
-
 # ------------------------------------------------------- tensor conveniences
-def cache_buffers(pages: int, H: int, page_size: int, D: int, k_format: int = SAGE_CACHE_INT8,
-                  v_format: int = SAGE_CACHE_E4M3, device="cuda"):
-    """An empty cache: (k, k_scale, v, v_scale), codes int8 or float8_e4m3fn
-    [pages, H, page_size, D], scales float32 [pages, H, page_size]."""
-    import torch
-    dt = {f: t for t, f in _formats().items()}
-    codes = lambda f: torch.empty((pages, H, page_size, D), dtype=dt[f], device=device)
-    scale = lambda: torch.empty((pages, H, page_size), dtype=torch.float32, device=device)
-    return codes(k_format), scale(), codes(v_format), scale()
-
-
 def quant_shapes(B: int, N: int, H: int, D: int) -> dict:
     """Shapes of the quantised buffers (layouts of include/sage_b200.h)."""
     Nq = -(-N // 128) * 128
@@ -600,3 +421,18 @@ def attention(q, k, v, out=None, sm_scale: float = 0.0, ws=None, stream=None):
         ws = workspace(SAGE_OP_ATTN_FWD, B, N, H, D, q.device)
     sage_attn_fwd(q, k, v, out, sm_scale, ws, stream)
     return out
+
+
+# ------------------------------------------- rotary positions and the cache
+_SERVING = ("sage_rope_freqs", "sage_rope", "sage_cache_append", "sage_cache_read", "sage_cache_attn",
+            "sage_clear_device_status", "cache_buffers")
+
+
+def __getattr__(name):
+    """The serving calls live in serving.py, which imports torch; they are
+    loaded on first use."""
+    if name in _SERVING:
+        from . import serving
+        globals().update({n: getattr(serving, n) for n in _SERVING})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
