@@ -39,26 +39,23 @@ __device__ __forceinline__ void rotate(float x0, float x1, float2 cs, float& y0,
 // One item of a head: item < rot_items rotates, the others copy 8 channels.
 // HALF: 8 pairs (8 channels of each half).  Interleaved: 4 pairs.
 template <bool HALF>
-__device__ __forceinline__ void rope_item(const uint16_t* x, uint16_t* y, int item,
-                                          int rot_items, int rot, const float2* __restrict__ cs) {
-  if (item >= rot_items) {
-    const int d = rot + 8 * (item - rot_items);
-    *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(x + d);
+__device__ __forceinline__ void rope_item(uint4 a, uint4 b, uint16_t* y, bool turn, int d, int rot,
+                                          const float2* __restrict__ cs) {
+  if (!turn) {
+    *reinterpret_cast<uint4*>(y + d) = a;
     return;
   }
-  const int d = 8 * item;
-  const uint4 a = *reinterpret_cast<const uint4*>(x + d);
   const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
   uint32_t yw[4];
   if (HALF) {
-    const uint4 b = *reinterpret_cast<const uint4*>(x + d + rot / 2);
     const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
     uint32_t zw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float y0, y1, z0, z1;
-      rotate(lo_bf16(aw[i]), lo_bf16(bw[i]), cs[d + 2 * i], y0, z0);
-      rotate(hi_bf16(aw[i]), hi_bf16(bw[i]), cs[d + 2 * i + 1], y1, z1);
+      const float4 c = *reinterpret_cast<const float4*>(cs + d + 2 * i);
+      rotate(lo_bf16(aw[i]), lo_bf16(bw[i]), make_float2(c.x, c.y), y0, z0);
+      rotate(hi_bf16(aw[i]), hi_bf16(bw[i]), make_float2(c.z, c.w), y1, z1);
       yw[i] = pack_bf16(y0, y1);
       zw[i] = pack_bf16(z0, z1);
     }
@@ -77,8 +74,8 @@ __device__ __forceinline__ void rope_item(const uint16_t* x, uint16_t* y, int it
 // The same for a rotated width that does not split into 16-byte vectors: one
 // pair, or one copied channel.
 template <bool HALF>
-__device__ __forceinline__ void rope_item_1(const uint16_t* x, uint16_t* y, int item,
-                                            int rot_items, int rot, const float2* __restrict__ cs) {
+__device__ __forceinline__ void rope_item_1(const uint16_t* x, uint16_t* y, int item, int rot_items, int rot,
+                                            const float2* __restrict__ cs) {
   if (item >= rot_items) {
     const int d = rot + (item - rot_items);
     y[d] = x[d];
@@ -91,41 +88,81 @@ __device__ __forceinline__ void rope_item_1(const uint16_t* x, uint16_t* y, int 
   y[d1] = f32_to_bf16_rn(y1);
 }
 
+// Where a token's rows begin: input and output of Q and of K.
+struct TokenRows {
+  int64_t x[2], y[2];
+};
+
 // grid (token groups of `toks`, head groups of `heads`); the tokens are the
-// B*N of the batch, the heads Q's Hq then K's.
+// B*N of the batch, the heads Q's Hq then K's.  A thread takes one item of
+// kRopeRows rows at a time, their loads issued together.
+constexpr int kRopeRows = 4;
 template <bool HALF, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int toks, int heads, int items,
                                                             int rot_items, int item_shift) {
-  extern __shared__ float2 cs[];  // [toks][rot / 2]
-  const int64_t tok0 = (int64_t)blockIdx.x * toks;
-  const int nt = (int)min((int64_t)toks, (int64_t)a.B * a.N - tok0);
-  const int half_rot = a.rot / 2;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  TokenRows* tokens = reinterpret_cast<TokenRows*>(rope_smem);       // [toks]
+  float2* cs = reinterpret_cast<float2*>(rope_smem + toks * sizeof(TokenRows));  // [toks][pitch]
+  const int half_rot = a.rot / 2, pitch = (half_rot + 1) & ~1;  // 16-byte reads of two
+  const unsigned tok0 = blockIdx.x * (unsigned)toks;
+  const int nt = (int)min((unsigned)toks, (unsigned)(a.B * a.N) - tok0);
   for (int i = threadIdx.x; i < nt * half_rot; i += kRopeThreads) {
-    const int64_t tok = tok0 + i / half_rot;
-    const int j = i % half_rot;
-    const int b = (int)(tok / a.N), n = (int)(tok % a.N);
-    const int pos = a.positions ? a.positions[b * a.pos_stride_b + n] : n;
+    const int t = i / half_rot, j = i - t * half_rot;
+    const unsigned b = (tok0 + t) / (unsigned)a.N, n = (tok0 + t) - b * a.N;
+    const int pos = a.positions ? a.positions[b * a.pos_stride_b + n] : (int)n;
     double turns = (double)pos * a.inv_freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
     turns -= rint(turns);
     float s, c;
     sincospif(2.0f * (float)turns, &s, &c);
-    cs[i] = make_float2(a.mscale * c, a.inverse ? -a.mscale * s : a.mscale * s);
+    cs[t * pitch + j] = make_float2(a.mscale * c, a.inverse ? -a.mscale * s : a.mscale * s);
+  }
+  for (int t = threadIdx.x; t < nt; t += kRopeThreads) {
+    const int64_t b = (tok0 + t) / (unsigned)a.N, n = (tok0 + t) - (unsigned)b * a.N;
+    tokens[t].x[0] = b * a.q.sb + n * a.q.sn;
+    tokens[t].y[0] = b * a.q.yb + n * a.q.yn;
+    tokens[t].x[1] = b * a.k.sb + n * a.k.sn;
+    tokens[t].y[1] = b * a.k.yb + n * a.k.yn;
   }
   __syncthreads();
   const int item = threadIdx.x & ((1 << item_shift) - 1);
   if (item >= items) return;
-  const int h0 = blockIdx.y * heads, nh = min(heads, a.Hq + a.Hk - h0);
-  for (int r = threadIdx.x >> item_shift; r < nt * nh; r += kRopeThreads >> item_shift) {
-    const int t = r / nh, h = h0 + r % nh;
-    const int64_t tok = tok0 + t;
-    const int64_t b = tok / a.N, n = tok % a.N;
-    const bool is_q = h < a.Hq;
-    const RopeSide& s = is_q ? a.q : a.k;
-    const int hh = is_q ? h : h - a.Hq;
-    const uint16_t* x = s.x + b * s.sb + n * s.sn + hh * s.sh;
-    uint16_t* y = s.y + b * s.yb + n * s.yn + hh * s.yh;
-    if (VEC) rope_item<HALF>(x, y, item, rot_items, a.rot, cs + t * half_rot);
-    else rope_item_1<HALF>(x, y, item, rot_items, a.rot, cs + t * half_rot);
+  const int h0 = blockIdx.y * heads, nh = min(heads, a.Hq + a.Hk - h0), n_rows = nt * nh;
+  const int step = kRopeThreads >> item_shift;
+  const bool turn = item < rot_items;
+  const int d = turn ? 8 * item : a.rot + 8 * (item - rot_items);
+  auto locate = [&](int r, const uint16_t*& x, uint16_t*& y, int& t) {
+    t = (unsigned)r / (unsigned)nh;
+    const int h = h0 + r - t * nh, is_k = h >= a.Hq;
+    const RopeSide& s = is_k ? a.k : a.q;
+    const int64_t hh = is_k ? h - a.Hq : h;
+    x = s.x + tokens[t].x[is_k] + hh * s.sh;
+    y = s.y + tokens[t].y[is_k] + hh * s.yh;
+  };
+  if (VEC) {
+    for (int r = threadIdx.x >> item_shift; r < n_rows; r += kRopeRows * step) {
+      uint4 u[kRopeRows], v[kRopeRows];
+      uint16_t* y[kRopeRows];
+      int t[kRopeRows];
+#pragma unroll
+      for (int k = 0; k < kRopeRows; ++k) {
+        if (r + k * step >= n_rows) continue;
+        const uint16_t* x;
+        locate(r + k * step, x, y[k], t[k]);
+        u[k] = *reinterpret_cast<const uint4*>(x + d);
+        if (HALF && turn) v[k] = *reinterpret_cast<const uint4*>(x + d + a.rot / 2);
+      }
+#pragma unroll
+      for (int k = 0; k < kRopeRows; ++k)
+        if (r + k * step < n_rows) rope_item<HALF>(u[k], v[k], y[k], turn, d, a.rot, cs + t[k] * pitch);
+    }
+  } else {
+    for (int r = threadIdx.x >> item_shift; r < n_rows; r += step) {
+      const uint16_t* x;
+      uint16_t* y;
+      int t;
+      locate(r, x, y, t);
+      rope_item_1<HALF>(x, y, item, rot_items, a.rot, cs + t * pitch);
+    }
   }
 }
 
@@ -146,7 +183,7 @@ void run(const RopeArgs& a, cudaStream_t s) {
   int heads = H;
   while (heads > 4 && groups * ((H + heads - 1) / heads) < 2 * 148) heads = (heads + 1) / 2;
   const dim3 grid((unsigned)groups, (H + heads - 1) / heads);
-  const size_t smem = (size_t)toks * (a.rot / 2) * sizeof(float2);
+  const size_t smem = (size_t)toks * (sizeof(TokenRows) + ((a.rot / 2 + 1) & ~1) * sizeof(float2));
   if (vec) rope_kernel<HALF, true><<<grid, kRopeThreads, smem, s>>>(a, toks, heads, items, rot_items, shift);
   else rope_kernel<HALF, false><<<grid, kRopeThreads, smem, s>>>(a, toks, heads, items, rot_items, shift);
 }
