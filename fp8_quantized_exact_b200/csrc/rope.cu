@@ -95,11 +95,15 @@ struct TokenRows {
 
 // grid (token groups of `toks`, head groups of `heads`); the tokens are the
 // B*N of the batch, the heads Q's Hq then K's.  A thread takes one item of
-// kRopeRows rows at a time, their loads issued together.
-constexpr int kRopeRows = 4;
+// ROWS rows at a time, their loads issued together: one row in the half layout,
+// whose items have two loads already, four in the interleaved one (measured on
+// B200 with 1, 2 and 4 rows: 343, 379, 399 us for the half layout at B1 N37810
+// 56+56 heads D128, 331 us at the copy rate; 141, 138, 135 us for the interleaved
+// one at B4 N16384 24+24 heads D64 rot 32, 123 us at the copy rate).
 template <bool HALF, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int toks, int heads, int items,
                                                             int rot_items, int item_shift) {
+  constexpr int ROWS = HALF ? 1 : 4;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   TokenRows* tokens = reinterpret_cast<TokenRows*>(rope_smem);       // [toks]
   float2* cs = reinterpret_cast<float2*>(rope_smem + toks * sizeof(TokenRows));  // [toks][pitch]
@@ -139,12 +143,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
     y = s.y + tokens[t].y[is_k] + hh * s.yh;
   };
   if (VEC) {
-    for (int r = threadIdx.x >> item_shift; r < n_rows; r += kRopeRows * step) {
-      uint4 u[kRopeRows], v[kRopeRows];
-      uint16_t* y[kRopeRows];
-      int t[kRopeRows];
+    for (int r = threadIdx.x >> item_shift; r < n_rows; r += ROWS * step) {
+      uint4 u[ROWS], v[ROWS];
+      uint16_t* y[ROWS];
+      int t[ROWS];
 #pragma unroll
-      for (int k = 0; k < kRopeRows; ++k) {
+      for (int k = 0; k < ROWS; ++k) {
         if (r + k * step >= n_rows) continue;
         const uint16_t* x;
         locate(r + k * step, x, y[k], t[k]);
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
         if (HALF && turn) v[k] = *reinterpret_cast<const uint4*>(x + d + a.rot / 2);
       }
 #pragma unroll
-      for (int k = 0; k < kRopeRows; ++k)
+      for (int k = 0; k < ROWS; ++k)
         if (r + k * step < n_rows) rope_item<HALF>(u[k], v[k], y[k], turn, d, a.rot, cs + t[k] * pitch);
     }
   } else {
