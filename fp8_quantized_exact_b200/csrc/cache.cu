@@ -22,42 +22,23 @@
 // a row, so that its lookups and scale cost little per element, and eight
 // neighbouring tokens of a head lie in one warp: their scales are one 32-byte
 // sector and their codes are contiguous in the page.
+#include "cache_codes.cuh"
 #include "cache_common.cuh"
 
 namespace sage {
 namespace {
+
+using cattn::add2;
+using cattn::fma2;
+using cattn::mul2;
+using cattn::pair;
+using cattn::unpair;
 
 constexpr int kCacheThreads = 256;
 
 constexpr int kLanes = 4;                          // threads of a row
 constexpr int kPerBlock = kCacheThreads / kLanes;  // rows of a block at a time
 
-// Two FP32 values in one 64-bit register.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));

@@ -29,6 +29,7 @@
 // end.  A tile is two boxes of 16 keys, the smallest page, so a box never crosses
 // one.
 #include "cache_attn.cuh"
+#include "cache_codes.cuh"
 #include "tc_prims.cuh"
 
 namespace sage {
@@ -37,34 +38,6 @@ namespace {
 using namespace cattn;
 
 constexpr int kTile = 32, kBox = 16;  // keys
-constexpr float kRaise = 8.0f;
-
-// Row of an 8-key block of an MMA operand -> key.  Keys of neighbouring rows
-// differ in bits 0 and 2, so the 16-byte shared-memory reads of two rows fall
-// on different banks under both swizzles (64- and 128-byte rows).
-__device__ __forceinline__ int key_of(int n) { return (n >> 1) ^ ((n & 1) ? 5 : 0); }
-
-// Four codes -> bytes 0 and 2, and bytes 1 and 3, as FP16 pairs.
-template <int F>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
-  if (F == SAGE_CACHE_INT8) {
-    // 0x6400 | (code + 128) is 1024 + 128 + code in FP16
-    const uint32_t e = (w & 0x00FF00FFu) ^ 0x64806480u, o = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(0x64806480u));
-  } else {
-    const uint32_t p = __byte_perm(w, 0, 0x3120);
-    asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi;}"
-        : "=r"(even), "=r"(odd)
-        : "r"(p));
-  }
-}
-
-// Unused slots hold any bytes: E4M3 NaN codes become 0 (their weight is 0).
-template <int F>
-__device__ __forceinline__ uint32_t no_nan(uint32_t w) {
-  return F == SAGE_CACHE_E4M3 ? w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) : w;
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -83,52 +56,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Two FP32 values in one 64-bit register (a row pair).
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-template <int D>
-__device__ __forceinline__ uint32_t swizzled(int key, int chunk) {
-  return key * D + ((D == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3)) << 4);
-}
-
 // Launch shape by the number of 8-row groups.  The registers leave room for a
 // block of the joining kernel beside the CTA.
 template <int D, int NT>
@@ -288,7 +215,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
         }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int eq = (top == 0 || top >= 0x7F80u) ? 0 : max((int)(top >> 7) - 127 - 13, -110);
+      const int eq = q_exponent(top);
       const float down = __int_as_float((127 - eq) << 23);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
@@ -296,7 +223,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
         put(s, make_uint2(pack_f16x2(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down),
                           pack_f16x2(__uint_as_float(w0 & 0xFFFF0000u) * down, __uint_as_float(w1 & 0xFFFF0000u) * down)));
       }
-      return fmaxf(a.sl2 * __int_as_float((127 + eq) << 23), 1.17549435e-38f);
+      return q_factor(a.sl2, eq);
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -622,6 +549,7 @@ int by_rows(const CacheAttnArgs& a, cudaStream_t s) {
 size_t cache_attn_workspace_bytes() { return kPartBytes; }
 
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
+  if (a.T * a.G > 16) return launch_cache_attn_tc(a, s);
   return a.c.D == 128 ? by_rows<128>(a, s) : by_rows<64>(a, s);
 }
 

@@ -1,0 +1,97 @@
+// Conversions and packed FP32 arithmetic shared by the cache's kernels.
+#pragma once
+#include "sage_common.cuh"
+
+namespace sage {
+namespace cattn {
+
+// Row of an 8-key block of an MMA operand -> key.  Keys of neighbouring rows
+// differ in bits 0 and 2, so the 16-byte shared-memory accesses of two rows fall
+// on different banks under both swizzles (64- and 128-byte rows).
+__device__ __forceinline__ int key_of(int n) { return (n >> 1) ^ ((n & 1) ? 5 : 0); }
+
+// Four codes -> bytes 0 and 2, and bytes 1 and 3, as FP16 pairs (exact).
+template <int F>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if (F == SAGE_CACHE_INT8) {
+    // 0x6400 | (code + 128) is 1024 + 128 + code in FP16
+    const uint32_t e = (w & 0x00FF00FFu) ^ 0x64806480u, o = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(0x64806480u));
+  } else {
+    const uint32_t p = __byte_perm(w, 0, 0x3120);
+    asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi;}"
+        : "=r"(even), "=r"(odd)
+        : "r"(p));
+  }
+}
+
+// Unused slots hold any bytes: E4M3 NaN codes become 0 (their weight is 0).
+template <int F>
+__device__ __forceinline__ uint32_t no_nan(uint32_t w) {
+  return F == SAGE_CACHE_E4M3 ? w & ~__vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) : w;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two FP32 values in one 64-bit register.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `key` of a tile of D-byte rows
+// that TMA wrote with the D-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int key, int chunk) {
+  return key * D + ((D == 128 ? chunk ^ (key & 7) : chunk ^ ((key >> 1) & 3)) << 4);
+}
+
+// The power of two by which a Q row is divided before it becomes FP16 (from the
+// largest magnitude's BF16 bits): its largest value then is below 2^14, and its
+// BF16 values are exact in FP16 down to 2^-27 of the largest.
+__device__ __forceinline__ int q_exponent(uint32_t top) {
+  return (top == 0 || top >= 0x7F80u) ? 0 : max((int)(top >> 7) - 127 - 13, -110);
+}
+// The factor of the row's raw scores (base 2).
+__device__ __forceinline__ float q_factor(float sl2, int eq) {
+  return fmaxf(sl2 * __int_as_float((127 + eq) << 23), 1.17549435e-38f);
+}
+
+constexpr float kRaise = 8.0f;  // a row's offset is raised for scores that pass it by more (log2)
+
+}  // namespace cattn
+}  // namespace sage

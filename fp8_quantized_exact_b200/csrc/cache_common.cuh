@@ -91,5 +91,6 @@ struct CacheAttnArgs {
 };
 size_t cache_attn_workspace_bytes();
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);
+int launch_cache_attn_tc(const CacheAttnArgs& a, cudaStream_t s);  // its variant for many rows per head
 
 }  // namespace sage
