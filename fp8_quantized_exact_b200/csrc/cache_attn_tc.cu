@@ -14,11 +14,11 @@
 //                    owns a row.  It also converts half of the row's Q at the
 //                    start of a unit and stores half of its output at the end, and
 //                    multiplies its O row when c or E is raised, which is rare.
-//   warps 8-11       converters: raw K and V codes of a tile -> FP16 tiles in the
+//   warps 8-15       converters: raw K and V codes of a tile -> FP16 tiles in the
 //                    128-byte swizzle that the MMAs read (K K-major, V MN-major).
-//   warp 12          TMA producer of raw tiles (four boxes of 16 keys each) and
-//                    of their scales (64-byte bulk copies).
-//   warp 13          MMA issuer: QK two tiles ahead of PV; P is the TMEM A operand.
+//   warps 16, 17     TMA producers of raw K and V tiles (one box per page that the
+//                    tile touches) and of their scales (bulk copies).
+//   warps 18, 19     QK and PV issuers; P is the TMEM A operand of PV.
 // Channels are in the order 0, 2, 1, 3 within each four, in Q, K and V alike, as the
 // conversion yields them; the output undoes it.
 //
@@ -34,12 +34,12 @@ namespace {
 using namespace cattn;
 using namespace tc;
 
-constexpr int kRowsT = 128, kTileT = 64, kBoxT = 16;
-constexpr int kConv0 = 8, kConvWarps = 4, kLoadWarpT = kConv0 + kConvWarps, kMmaWarpT = kLoadWarpT + 1;
-constexpr int kThreadsT = 32 * (kMmaWarpT + 1);
-constexpr int kAhead = 2;      // tiles that QK runs ahead of PV
+constexpr int kRowsT = 128, kTileT = 64;
+constexpr int kConv0 = 8, kConvWarps = 8, kLoadK = kConv0 + kConvWarps, kLoadV = kLoadK + 1, kQkWarpT = kLoadK + 2,
+              kPvWarpT = kLoadK + 3;
+constexpr int kThreadsT = 32 * (kPvWarpT + 1);
 constexpr int kKStages = 2, kVStages = 4;
-constexpr int kScales = 16;    // scale ring: a tile's slot is free when 9 more tiles have been issued
+constexpr int kScales = 16;    // scale ring: softmax has read a tile's slot before its successor's loads are issued
 constexpr uint32_t kColsT = 512, kColOT = 256;  // TMEM: S buffers [stream][2] of 64 columns, then O of each stream
 
 template <int D>
@@ -50,18 +50,22 @@ struct SmemT {
   alignas(1024) uint8_t v[kVStages][kTileT * D * 2];
   alignas(1024) uint8_t raw[kRaw][2][kTileT * D];
   alignas(128) float scale[kScales][2][kTileT];
-  alignas(16) float vd[8][kTileT];      // per softmax warp: V scales times 2^-E
+  alignas(16) float vd[kScales][kTileT];  // V scales times 2^-E of the tile (tiles that every row sees whole)
+  int e[kScales];                       // that E
   uint32_t amax[2][kRowsT];             // of the halves of Q's rows
   float c[2][kRowsT], l[2][kRowsT], up[2][kRowsT];  // what the streams exchange at a unit's end
-  int flags[kScales];                   // bits 0-3: the boxes that hold keys; bit 4: not every row sees every key
+  int flags[kScales];                   // bits 0-3: the 16-key groups that hold keys; bit 4: not every row sees every key; bit 5: a unit's first tile
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2][2], p_full[2], o_done[2];
-  uint64_t q_full, swap, drain;
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [stream][its tiles mod 2]
+  uint64_t q_full, swap, drain[2];
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr int kMasked = 16;
+constexpr int kMasked = 16, kFirst = 32;
+
+// E for a largest V scale, by its bits (NaN left out by the callers): 2^E is above it.
+__device__ __forceinline__ int v_exponent(uint32_t bits) { return min((int)(bits >> 23) - 126, 126); }
 
 // Descriptor of a 128-byte-swizzled tile: `lbo` and `sbo` in bytes.
 __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -72,24 +76,31 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lbo, uint32_
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool mn) {
   return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRowsT >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The issuing warps run converged and predicate the instruction itself on the
+// one lane `on`, so that the operands stay in uniform registers: inside a branch
+// on the lane each MMA took about 80 cycles to issue.
+__device__ __forceinline__ void mma_f16_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a),
-      "l"(b), "r"(idesc), "r"(accumulate)
+      "{.reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{.reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
-// After the wait for loads: no use of the registers moves before it.
-template <int N>
-__device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+__device__ __forceinline__ void commit(uint32_t on, uint64_t* b) {
+  asm volatile(
+      "{.reg .pred q; setp.ne.b32 q, %1, 0;"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];}" ::"r"(smem_u32(b)),
+      "r"(on)
+      : "memory");
 }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -103,26 +114,27 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One 64-key tile of raw codes -> FP16 in the MMA layout: 64-channel blocks of
-// [key][128 bytes].  Warp w of the converters takes the keys 16 w .. 16 w + 15.
+// [key][128 bytes].  Warp w of the converters takes the keys 8 w .. 8 w + 7.
 template <int D, int F>
 __device__ __forceinline__ void convert(uint32_t raw, uint32_t to, int w, int lane, bool clean) {
-  const int c = lane & 3;
+  const int c = lane & 3, key = 8 * w + key_of(lane >> 2);
+  uint4 in[D / 64];
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb) {
-    const int key = 16 * w + 8 * kb + key_of(lane >> 2);
-    uint4 in[D / 64];
+  for (int x = 0; x < D / 64; ++x) in[x] = lds128(raw + swizzled<D>(key, 4 * x + c));
+  if (F == SAGE_CACHE_E4M3 && clean) {
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) in[x] = lds128(raw + swizzled<D>(key, 4 * x + c));
+    for (int x = 0; x < D / 64; ++x)
+      in[x] = make_uint4(no_nan<F>(in[x].x), no_nan<F>(in[x].y), no_nan<F>(in[x].z), no_nan<F>(in[x].w));
+  }
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x) {
-      uint32_t o[8];
-      const uint32_t iw[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+  for (int x = 0; x < D / 64; ++x) {
+    uint32_t o[8];
+    const uint32_t iw[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) codes_to_f16<F>(clean ? no_nan<F>(iw[e]) : iw[e], o[2 * e], o[2 * e + 1]);
-      const uint32_t row = to + x * (kTileT * 128) + key * 128;
-      sts128(row + (((2 * c) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
-      sts128(row + (((2 * c + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
-    }
+    for (int e = 0; e < 4; ++e) codes_to_f16<F>(iw[e], o[2 * e], o[2 * e + 1]);
+    const uint32_t row = to + x * (kTileT * 128) + key * 128;
+    sts128(row + (((2 * c) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
+    sts128(row + (((2 * c + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NR; ++s) {
-      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_full[s], 2);  // both producers
       mbar_init(&sm.raw_empty[s], kConvWarps);
     }
     for (int s = 0; s < kKStages; ++s) {
@@ -162,18 +174,20 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       mbar_init(&sm.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.s_full[s][0], 1);
-      mbar_init(&sm.s_full[s][1], 1);
-      mbar_init(&sm.p_full[s], 4);
-      mbar_init(&sm.o_done[s], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&sm.s_full[s][k], 1);
+        mbar_init(&sm.p_full[s][k], 4);
+        mbar_init(&sm.o_done[s][k], 1);
+      }
     }
     mbar_init(&sm.q_full, 256);
     mbar_init(&sm.swap, 256);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarpT) tmem_alloc(&sm.tmem_base, kColsT);
+  if (warp == kQkWarpT) tmem_alloc(&sm.tmem_base, kColsT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -241,10 +255,114 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         mbar_arrive(&sm.q_full);
       }
       const uint64_t f2 = pair(f, f);
-      float c = 0.0f, thr = -INFINITY;
+      float c = 0.0f;
+      bool none = true;  // nothing seen yet
       uint64_t l0 = 0, l1 = 0;
       int E = -126;
       bool fresh = true;  // no PV of this unit yet: the accumulator holds nothing
+
+      // one tile; first and later ones, seen whole by every row or masked
+      auto tile = [&](auto masked_tag, uint32_t cols, int slot, int k, uint64_t seen, int E_new) {
+        constexpr bool MASKED = decltype(masked_tag)::value;
+        const float* ks = sm.scale[slot][0];
+        const float* vs = MASKED ? sm.scale[slot][1] : sm.vd[slot];
+        const float down = __int_as_float((127 - E_new) << 23);
+        // c is raised until a row has seen something, with E, and where the sum of a tile's p passes 2^14 (so that FP16 holds each of
+        // them); the tile is then done again
+        bool raise = MASKED || __any_sync(0xffffffffu, none || E_new != E);
+        uint32_t p[32];
+        uint64_t s0, s1;
+        for (;;) {
+          uint32_t sa[16], sb[16];
+          if (raise) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j0 = 0; j0 < 64; j0 += 16) {
+              tmem_ld16(cols + j0, sa);
+              tmem_wait_ld16(sa);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                const float4 kk = *reinterpret_cast<const float4*>(ks + j0 + j);
+                const float x[4] = {__uint_as_float(sa[j]) * kk.x, __uint_as_float(sa[j + 1]) * kk.y,
+                                    __uint_as_float(sa[j + 2]) * kk.z, __uint_as_float(sa[j + 3]) * kk.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!MASKED || (seen >> (j0 + j + e)) & 1) top = fmaxf(top, x[e]);
+              }
+            }
+            const float c_new = none ? (top == -INFINITY ? 0.0f : top * f) : fmaxf(c, top * f);
+            const float al = none ? 0.0f : ex2(c - c_new), al_o = E_new == E ? al : al * ex2((float)(E - E_new));
+            none = none && top == -INFINITY;
+            c = c_new;
+            E = E_new;
+            l0 = mul2(l0, pair(al, al));
+            l1 = mul2(l1, pair(al, al));
+            if (!fresh && __any_sync(0xffffffffu, al_o != 1.0f)) {
+              // the PV before is done first, then the accumulator's row is multiplied
+              if (!(ok = wait(&sm.o_done[sid][(k - 1) & 1], (k - 1) >> 1, 3))) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int x = 0; x < D; x += 16) {
+                tmem_ld16(col_o + x, sa);
+                tmem_wait_ld16(sa);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sa[e] = __float_as_uint(__uint_as_float(sa[e]) * al_o);
+                tmem_st16(col_o + x, sa);
+              }
+            }
+          }
+          const uint64_t nc2 = pair(-c, -c);
+          s0 = s1 = 0;
+          // 16 keys from j0 on
+          auto chunk = [&](const uint32_t (&sr)[16], int j0) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 kk = *reinterpret_cast<const float4*>(ks + j0 + j);
+              float4 v = *reinterpret_cast<const float4*>(vs + j0 + j);
+              uint64_t x0 = mul2(pair(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), pair(kk.x, kk.y));
+              uint64_t x1 = mul2(pair(__uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3])), pair(kk.z, kk.w));
+              x0 = fma2(x0, f2, nc2);
+              x1 = fma2(x1, f2, nc2);
+              float2 a0 = unpair(x0), a1 = unpair(x1);
+              if (MASKED) {
+                const uint32_t on = (uint32_t)(seen >> (j0 + j));
+                if (!(on & 1)) { a0.x = -INFINITY; v.x = 0.0f; }
+                if (!(on & 2)) { a0.y = -INFINITY; v.y = 0.0f; }
+                if (!(on & 4)) { a1.x = -INFINITY; v.z = 0.0f; }
+                if (!(on & 8)) { a1.y = -INFINITY; v.w = 0.0f; }
+                v.x *= down; v.y *= down; v.z *= down; v.w *= down;
+              }
+              const uint64_t p0 = pair(ex2(a0.x), ex2(a0.y)), p1 = pair(ex2(a1.x), ex2(a1.y));
+              s0 = add2(s0, p0);
+              s1 = add2(s1, p1);
+              const float2 w0 = unpair(mul2(p0, pair(v.x, v.y))), w1 = unpair(mul2(p1, pair(v.z, v.w)));
+              p[(j0 + j) / 2] = pack_f16x2(w0.x, w0.y);
+              p[(j0 + j) / 2 + 1] = pack_f16x2(w1.x, w1.y);
+            }
+          };
+          tmem_ld16(cols, sa);
+          tmem_wait_ld16(sa);
+          tmem_ld16(cols + 16, sb);
+          chunk(sa, 0);
+          tmem_wait_ld16(sb);
+          tmem_ld16(cols + 32, sa);
+          chunk(sb, 16);
+          tmem_wait_ld16(sa);
+          tmem_ld16(cols + 48, sb);
+          chunk(sa, 32);
+          tmem_wait_ld16(sb);
+          chunk(sb, 48);
+          if (raise) break;
+          const float2 y = unpair(add2(s0, s1));
+          raise = __any_sync(0xffffffffu, !(y.x + y.y <= 16384.0f));
+          if (!raise) break;
+        }
+        l0 = add2(l0, s0);
+        l1 = add2(l1, s1);
+        tmem_st16(cols, *reinterpret_cast<const uint32_t(*)[16]>(&p[0]));
+        tmem_st16(cols + 16, *reinterpret_cast<const uint32_t(*)[16]>(&p[16]));
+        tmem_wait_st();
+      };
 
       // ---- tiles of this stream
       int i = (int)(seg - st.s);
@@ -255,28 +373,13 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         tc_fence_after();
         const uint32_t cols = lanes + (sid * 2 + buf) * 64;
         if (!idle) {
-          uint32_t sr[64];
-          tmem_ld64(cols, sr);
-          const float* ks = sm.scale[slot][0];
-          const float* vs = sm.scale[slot][1];
           const int flags = sm.flags[slot];
-          const bool masked = flags & kMasked;
-          uint64_t seen = ~0ull;
-          float down = 0.0f;
-          int E_new = E;
-          if (!masked) {
-            const float v0 = vs[lane], v1 = vs[lane + 32];
-            const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(v0, v1), 0.0f)));
-            E_new = min(max(E, (int)(vm >> 23) - 126), 126);
-            down = __int_as_float((127 - E_new) << 23);
-            __syncwarp();
-            vd[lane] = v0 * down;
-            vd[lane + 32] = v1 * down;
-            __syncwarp();
+          if (!(flags & kMasked)) {
+            tile(std::false_type{}, cols, slot, k, ~0ull, sm.e[slot]);
           } else {
             const int64_t slot0 = (int64_t)(st.s + i - u.start) * kTileT;
             const int64_t d0 = slot0 - ctx;  // drafted token of the tile's first key (below 0: context)
-            seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
+            uint64_t seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
             if (row < rows && d0 < cnt && d0 > -64) {
               const int lo = (int)max(d0, (int64_t)0), hi = min((int)(d0 + 64), cnt);  // drafted tokens [lo, hi)
               uint64_t bits = 0;  // of tokens lo, lo + 1, ...
@@ -298,93 +401,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
               if (!((flags >> x) & 1)) seen &= ~(0xFFFFull << (16 * x));
             float vm = 0.0f;
             for (int j = 0; j < 64; ++j)
-              if ((seen >> j) & 1) vm = fmaxf(vm, vs[j]);
-            E_new = min(max(E, (__float_as_int(vm) >> 23) - 126), 126);
-            down = __int_as_float((127 - E_new) << 23);
+              if ((seen >> j) & 1) vm = fmaxf(vm, sm.scale[slot][1][j]);
+            tile(std::true_type{}, cols, slot, k, seen, max(E, v_exponent(__float_as_uint(vm))));
           }
-          loaded(sr);
-          float top = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float4 kk = *reinterpret_cast<const float4*>(ks + j);
-            const float2 x = unpair(mul2(pair(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), pair(kk.x, kk.y)));
-            const float2 y = unpair(mul2(pair(__uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3])), pair(kk.z, kk.w)));
-            sr[j] = __float_as_uint(x.x); sr[j + 1] = __float_as_uint(x.y);
-            sr[j + 2] = __float_as_uint(y.x); sr[j + 3] = __float_as_uint(y.y);
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (!((seen >> j) & 1)) sr[j] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) top = fmaxf(top, fmaxf(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])));
-          const bool up = top > thr || E_new != E;
-          if (__any_sync(0xffffffffu, up)) {
-            const bool none = thr == -INFINITY;
-            const float c_new = none ? (top == -INFINITY ? 0.0f : top * f) : fmaxf(c, top * f);
-            const float al = none ? 0.0f : ex2(c - c_new);
-            if (top != -INFINITY && (none || c_new > c)) thr = top + kRaise / f;
-            const float al_o = E_new == E ? al : al * ex2((float)(E - E_new));
-            c = c_new;
-            E = E_new;
-            l0 = mul2(l0, pair(al, al));
-            l1 = mul2(l1, pair(al, al));
-            if (!fresh && __any_sync(0xffffffffu, al_o != 1.0f)) {
-              // the scores wait in registers while the accumulator's row is multiplied
-              if (!(ok = wait(&sm.o_done[sid], k - 1, 3))) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int x = 0; x < D; x += 16) {
-                uint32_t o[16];
-                tmem_ld16(col_o + x, o);
-                tmem_wait_ld16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al_o);
-                tmem_st16(col_o + x, o);
-              }
-            }
-          }
-          const uint64_t nc2 = pair(-c, -c);
-          uint32_t p[32];
-#pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const float2 x = unpair(fma2(pair(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), f2, nc2));
-            const float2 y = unpair(fma2(pair(__uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3])), f2, nc2));
-            const uint64_t px = pair(ex2(x.x), ex2(x.y)), py = pair(ex2(y.x), ex2(y.y));
-            l0 = add2(l0, px);
-            l1 = add2(l1, py);
-            float4 v;
-            if (!masked) {
-              v = *reinterpret_cast<const float4*>(vd + j);
-            } else {
-              v = *reinterpret_cast<const float4*>(vs + j);
-              v.x = (seen >> j) & 1 ? v.x * down : 0.0f;
-              v.y = (seen >> (j + 1)) & 1 ? v.y * down : 0.0f;
-              v.z = (seen >> (j + 2)) & 1 ? v.z * down : 0.0f;
-              v.w = (seen >> (j + 3)) & 1 ? v.w * down : 0.0f;
-            }
-            const float2 wx = unpair(mul2(px, pair(v.x, v.y))), wy = unpair(mul2(py, pair(v.z, v.w)));
-            p[j / 2] = pack_f16x2(wx.x, wx.y);
-            p[j / 2 + 1] = pack_f16x2(wy.x, wy.y);
-          }
-          tmem_st16(cols, *reinterpret_cast<const uint32_t(*)[16]>(&p[0]));
-          tmem_st16(cols + 16, *reinterpret_cast<const uint32_t(*)[16]>(&p[16]));
-          tmem_wait_st();
+          if (!ok) break;
         }
         fresh = false;
-        // one tile's P at a time: the PV before has been seen, so the phases of p_full and o_done stay next to those waited for
-        if (k >= 1 && !(ok = wait(&sm.o_done[sid], k - 1, 1))) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[sid]);
+        if (lane == 0) mbar_arrive(&sm.p_full[sid][buf]);
       }
       if (!ok) break;
 
       // ---- the unit's end: wait for this stream's last PV, exchange the states, store half of the columns
       if (!fresh) {
         const int last = ((int)(seg_end - st.s) - 1 - sid) >> 1;  // the stream's tile before the end
-        if (!(ok = wait(&sm.o_done[sid], last, 4))) break;
+        if (!(ok = wait(&sm.o_done[sid][last & 1], last >> 1, 4))) break;
       }
       float l;
       {
@@ -392,7 +424,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         l = (x.x + x.y) + (y.x + y.y);
       }
       sm.l[sid][row] = l;
-      sm.c[sid][row] = thr == -INFINITY ? -INFINITY : c;
+      sm.c[sid][row] = none ? -INFINITY : c;
       sm.up[sid][row] = fresh ? 0.0f : __int_as_float((127 + E) << 23);  // 2^E; 0: the accumulator holds nothing
       tc_fence_before();
       mbar_arrive(&sm.swap);
@@ -444,13 +476,26 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       tc_fence_before();
       seg = seg_end;
     }
-  } else if (warp < kLoadWarpT) {
+  } else if (warp < kLoadK) {
     // ----------------------------------------------------------- converters
     const int w = warp - kConv0;
+    int E = -126;  // of the tiles so far that every row sees whole
     for (int i = 0; i < n_tiles; ++i) {
-      const int r = i % NR;
+      const int r = i % NR, slot = i & (kScales - 1);
       if (!wait(&sm.raw_full[r], i / NR, 6)) break;
-      const bool clean = sm.flags[i & (kScales - 1)] & kMasked;
+      const int flags = sm.flags[slot];
+      const bool clean = flags & kMasked;
+      if (w == 0) {
+        if (flags & kFirst) E = -126;
+        if (!clean) {
+          const float v0 = sm.scale[slot][1][lane], v1 = sm.scale[slot][1][lane + 32];
+          E = max(E, v_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(v0, v1), 0.0f)))));
+          const float down = __int_as_float((127 - E) << 23);
+          sm.vd[slot][lane] = v0 * down;
+          sm.vd[slot][lane + 32] = v1 * down;
+          if (lane == 0) sm.e[slot] = E;
+        }
+      }
       if (!wait(&sm.k_empty[i % kKStages], (i / kKStages) ^ 1, 7)) break;
       convert<D, KF>(smem_u32(sm.raw[r][0]), smem_u32(sm.k[i % kKStages]), w, lane, false);
       fence_async_smem();
@@ -465,12 +510,15 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         mbar_arrive(&sm.raw_empty[r]);
       }
     }
-  } else if (warp == kLoadWarpT) {
-    // ------------------------------------------------------------- producer
-    // lane 4 t + x looks up box x of tile t of the next eight
+  } else if (warp <= kLoadV) {
+    // ------------------------------------------------------------ producers
+    // A tile's boxes are 16, 32 or 64 keys, what a page holds of it.  Lane 4 t + x looks up the row of group x of 16 keys
+    // of tile t of the next eight; the first group of a box stands for it.
+    const int side = warp - kLoadK, box = min(1 << a.c.page_shift, kTileT), per = box / 16;
+    const CUtensorMap* map = side ? &tm_v : &tm_k;
     Place walk = place_of<kTileT, kRowsT>(a, st.s);
     int issued = 0, rows8 = -1;
-    bool masked8 = false;
+    bool masked8 = false, first8 = false;
     for (int i = 0; i < n_tiles; ++i) {
       const int r = i % NR, slot = i & (kScales - 1);
       if ((i & 7) == 0) {
@@ -480,8 +528,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         if (idx < st.e) {
           go_to<kTileT, kRowsT>(a, walk, idx);
           const Unit u = unit_of(walk, idx);
-          const int64_t first = (int64_t)(idx - u.start) * kTileT, s = first + kBoxT * (lane & 3);
+          const int64_t first = (int64_t)(idx - u.start) * kTileT, s = first + 16 * (lane & 3);
           masked8 = first + kTileT > walk.s.ctx;
+          first8 = idx == max(u.start, st.s);
           if (s < (int64_t)walk.s.ctx + walk.s.cnt) {
             rows8 = (int)cache_row(a.c, walk.b, u.h, s);
             if (rows8 < 0) flag_bad(status, kWhereAttn);
@@ -490,110 +539,84 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       const int row = __shfl_sync(0xffffffffu, rows8, 4 * (i & 7) + (lane & 3));
       const bool masked = __shfl_sync(0xffffffffu, masked8, 4 * (i & 7));
+      const bool begins = __shfl_sync(0xffffffffu, first8, 4 * (i & 7));
       const uint32_t valid = __ballot_sync(0xffffffffu, lane < 4 && row >= 0);
-      const bool ok = wait(&sm.raw_empty[r], (i / NR) ^ 1, 9);
-      __syncwarp();
-      if (!ok) break;
+      const uint32_t boxes = __ballot_sync(0xffffffffu, lane < 4 && row >= 0 && lane % per == 0);
+      if (!wait(&sm.raw_empty[r], (i / NR) ^ 1, 9)) break;
       if (lane == 0) {
-        sm.flags[slot] = (int)valid | (masked || valid != 15u ? kMasked : 0);
-        mbar_expect_tx(&sm.raw_full[r], __popc(valid) * (2 * kBoxT * D + 2 * kBoxT * 4));
+        if (side == 0) sm.flags[slot] = (int)valid | (masked || valid != 15u ? kMasked : 0) | (begins ? kFirst : 0);
+        mbar_expect_tx(&sm.raw_full[r], __popc(boxes) * box * (D + 4));
       }
       __syncwarp();
-      if (lane < 4 && row >= 0) {
-        tma_load_3d(sm.raw[r][0] + lane * kBoxT * D, &tm_k, 0, row, 0, &sm.raw_full[r]);
-        tma_load_3d(sm.raw[r][1] + lane * kBoxT * D, &tm_v, 0, row, 0, &sm.raw_full[r]);
-        bulk_load(&sm.scale[slot][0][lane * kBoxT], a.c.scale[0] + row, kBoxT * 4, &sm.raw_full[r]);
-        bulk_load(&sm.scale[slot][1][lane * kBoxT], a.c.scale[1] + row, kBoxT * 4, &sm.raw_full[r]);
+      if ((boxes >> lane) & 1u) {
+        tma_load_3d(sm.raw[r][side] + lane * 16 * D, map, 0, row, 0, &sm.raw_full[r]);
+        bulk_load(&sm.scale[slot][side][lane * 16], a.c.scale[side] + row, box * 4, &sm.raw_full[r]);
       }
       issued = i + 1;
     }
     for (int i = max(0, issued - NR); i < issued; ++i)
       wait_bounded(&sm.raw_full[i % NR], (uint32_t)((i / NR) & 1), abort_flag, nullptr, 110, kDefaultWaitLimit, false);
   } else {
-    // ----------------------------------------------------------- MMA issuer
-    const bool leader = lane == 0;
-    constexpr uint32_t iqk = idesc_f16(kTileT, false), ipv = idesc_f16(D, true);
-    const uint64_t qd = desc128(smem_u32(sm.q), 16, 1024);
+    // -------------------------------------------------------------- issuers
+    const uint32_t leader = lane == 0;
     Place at = place_of<kTileT, kRowsT>(a, st.s);
-    unsigned seg_end = st.s;   // of the unit that tile i belongs to
-    int units = 0, pv = 0, pv_first = 0;
-    int seen[2] = {0, 0};  // PVs of each stream known to be done
-    bool ok = true;
-    // PV of tile j, whose unit's tiles begin at pv_first
-    auto issue_pv = [&](int j) {
-      const int s = j & 1, k = j >> 1;
-      ok = wait(&sm.p_full[s], k, 11) && wait(&sm.v_full[j % kVStages], j / kVStages, 12);
-      __syncwarp();
-      if (!ok) return;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t vdsc = desc128(smem_u32(sm.v[j % kVStages]), BLK, 1024);
-        const uint32_t p = tmem + (s * 2 + (k & 1)) * 64, o = tmem + kColOT + s * D;
-#pragma unroll
-        for (int x = 0; x < kTileT / 16; ++x)
-          mma_f16_ts(o, p + 8 * x, vdsc + x * (2048 >> 4), ipv, (j >= pv_first + 2 || x > 0) ? 1u : 0u);
-        tc_commit(&sm.o_done[s]);
-        tc_commit(&sm.v_empty[j % kVStages]);
-      }
-      __syncwarp();
-    };
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      if (st.s + i == seg_end) {  // a new unit: finish the one before, then wait for its Q
-        for (; ok && pv < i; ++pv) issue_pv(pv);
-        if (!ok) break;
+    unsigned seg_end = st.s;  // of the unit that tile i belongs to
+    int units = 0, begin = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int s = i & 1, k = i >> 1;
+      const uint32_t sc = tmem + (s * 2 + (k & 1)) * 64;
+      const bool next = st.s + i == seg_end;
+      if (next) {
         go_to<kTileT, kRowsT>(a, at, st.s + i);
         const Unit u = unit_of(at, st.s + i);
         seg_end = min(u.start + at.s.n, st.e);
-        pv_first = i;
-        ok = wait(&sm.q_full, units++, 13);
-        __syncwarp();
-        if (!ok) break;
-        seen[0] = (i + 1) >> 1;  // the streams wrote Q after their last PV
-        seen[1] = i >> 1;
+        begin = i;
       }
-      const int s = i & 1, k = i >> 1;
-      // S buffer k & 1 of the stream: PV of the tile two back in the stream has read its P (of the PV behind that one,
-      // none is done yet unless a unit ended)
-      ok = (k < 2 || (s ? seen[1] : seen[0]) >= k - 1 || wait(&sm.o_done[s], k - 2, 14)) &&
-           wait(&sm.k_full[i % kKStages], i / kKStages, 15);
-      __syncwarp();
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t kd = desc128(smem_u32(sm.k[i % kKStages]), 16, 1024);
+      if (warp == kQkWarpT) {
+        // a new unit's Q; S buffer k & 1 of the stream: PV of the tile two back in the stream has read its P
+        if (next && !wait(&sm.q_full, units++, 13)) break;
+        if (k >= 2 && !wait(&sm.o_done[s][k & 1], (k >> 1) - 1, 14)) break;
+        if (!wait(&sm.k_full[i % kKStages], i / kKStages, 15)) break;
+        tc_fence_after();
+        const uint64_t qd = desc128(smem_u32(sm.q), 16, 1024), kd = desc128(smem_u32(sm.k[i % kKStages]), 16, 1024);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
-          mma_f16_ss(tmem + (s * 2 + (k & 1)) * 64, qd + (x / 4) * ((kRowsT * 128) >> 4) + 2 * (x % 4),
-                     kd + (x / 4) * (BLK >> 4) + 2 * (x % 4), iqk, x > 0);
-        tc_commit(&sm.s_full[s][k & 1]);
-        tc_commit(&sm.k_empty[i % kKStages]);
-      }
-      __syncwarp();
-      if (i - pv >= kAhead) {
-        issue_pv(pv);
-        ++pv;
+          mma_f16_ss(leader, sc, qd + (x / 4) * ((kRowsT * 128) >> 4) + 2 * (x % 4),
+                     kd + (x / 4) * (BLK >> 4) + 2 * (x % 4), idesc_f16(kTileT, false), x > 0);
+        commit(leader, &sm.s_full[s][k & 1]);
+        commit(leader, &sm.k_empty[i % kKStages]);
+      } else {
+        if (!wait(&sm.v_full[i % kVStages], i / kVStages, 12) || !wait(&sm.p_full[s][k & 1], k >> 1, 11)) break;
+        tc_fence_after();
+        const uint64_t vd = desc128(smem_u32(sm.v[i % kVStages]), BLK, 1024);
+        const uint32_t o = tmem + kColOT + s * D, more = i >= begin + 2;  // the unit's first tile of a stream starts its O
+#pragma unroll
+        for (int x = 0; x < kTileT / 16; ++x)
+          mma_f16_ts(leader, o, sc + 8 * x, vd + x * (2048 >> 4), idesc_f16(D, true), x > 0 ? 1u : more);
+        commit(leader, &sm.o_done[s][k & 1]);
+        commit(leader, &sm.v_empty[i % kVStages]);
       }
     }
-    for (; ok && pv < n_tiles; ++pv) issue_pv(pv);
     __syncwarp();
-    if (leader) tc_commit(&sm.drain);
-    __syncwarp();
-    wait_bounded(&sm.drain, 0, abort_flag, nullptr, 116, kDefaultWaitLimit, false);
+    uint64_t* drain = &sm.drain[warp - kQkWarpT];
+    commit(leader, drain);
+    wait_bounded(drain, 0, abort_flag, nullptr, 116, kDefaultWaitLimit, false);
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarpT) tmem_free(tmem, kColsT);
+  if (warp == kQkWarpT) tmem_free(tmem, kColsT);
 }
 
 template <int D, int KF, int VF>
 int launch_tc(const CacheAttnArgs& a, cudaStream_t s) {
   if (!list_fits<kTileT, kRowsT>(a)) return SAGE_ERR_UNSUPPORTED;
   const uint64_t rows = (uint64_t)a.c.pages * a.c.H << a.c.page_shift;
+  const uint32_t box = a.c.page_shift < 6 ? 1u << a.c.page_shift : kTileT;
   CUtensorMap mk, mv;
-  if (!make_map(&mk, a.c.codes[0], D, rows, 1, D, rows * D, D, kBoxT) ||
-      !make_map(&mv, a.c.codes[1], D, rows, 1, D, rows * D, D, kBoxT))
+  if (!make_map(&mk, a.c.codes[0], D, rows, 1, D, rows * D, D, box) ||
+      !make_map(&mv, a.c.codes[1], D, rows, 1, D, rows * D, D, box))
     return SAGE_ERR_CUDA;
   auto* fn = cache_attn_tc_kernel<D, KF, VF>;
   // more than half of an SM's shared memory: one CTA (and one request for all of the TMEM) per SM
