@@ -10,20 +10,26 @@
 //   warps 0-3, 4-7   two independent softmax streams, on alternate tiles, each
 //                    with its own O accumulator and its own c, l and E (joined at the
 //                    end of the unit, like split keys): one stream's softmax runs
-//                    beside the other's MMAs and nothing is handed over.  A thread
-//                    owns a row.  It also converts half of the row's Q at the
-//                    start of a unit and stores half of its output at the end, and
-//                    multiplies its O row when c or E is raised, which is rare.
-//   warps 8-15       converters: raw K and V codes of a tile -> FP16 tiles in the
-//                    128-byte swizzle that the MMAs read (K K-major, V MN-major).
+//                    beside the other's MMAs and nothing is handed over.  They work on
+//                    S in MMA fragment order (a quarter of the keys of four rows
+//                    per thread), write Q (half a row each) to TMEM at the start of a
+//                    unit, store half of the output each at its end, and multiply their
+//                    O rows when c or E is raised, which is rare.
+//   warps 8-11       converters of K: raw codes of a tile -> an FP16 tile in the
+//   warps 12-15      and of V: 128-byte swizzle that the MMAs read (V MN-major).
 //   warps 16, 17     TMA producers of raw K and V tiles (one box per page that the
 //                    tile touches) and of their scales (bulk copies).
-//   warps 18, 19     QK and PV issuers; P is the TMEM A operand of PV.
+//   warps 18, 19     QK and PV issuers.  The A operands, Q and P, are in TMEM: what
+//                    bounds the kernel is shared-memory bandwidth (raw tile in and
+//                    out, FP16 tile in and out: 112 KB per tile at D = 128, about 900
+//                    cycles; with Q in shared memory it was 144 KB).
 // Channels are in the order 0, 2, 1, 3 within each four, in Q, K and V alike, as the
 // conversion yields them; the output undoes it.
 //
 // Every wait is bounded; one that runs out records SAGE_ERR_TIMEOUT, raises the
 // CTA's abort flag, and every role leaves its loop and drains what it has in flight.
+#include <type_traits>
+
 #include "cache_attn.cuh"
 #include "cache_codes.cuh"
 #include "tc_prims.cuh"
@@ -35,17 +41,17 @@ using namespace cattn;
 using namespace tc;
 
 constexpr int kRowsT = 128, kTileT = 64;
-constexpr int kConv0 = 8, kConvWarps = 8, kLoadK = kConv0 + kConvWarps, kLoadV = kLoadK + 1, kQkWarpT = kLoadK + 2,
-              kPvWarpT = kLoadK + 3;
+constexpr int kConvK = 8, kConvV = 12, kConvWarps = 4, kLoadK = 16, kLoadV = 17, kQkWarpT = 18, kPvWarpT = 19;
 constexpr int kThreadsT = 32 * (kPvWarpT + 1);
 constexpr int kKStages = 2, kVStages = 4;
 constexpr int kScales = 16;    // scale ring: softmax has read a tile's slot before its successor's loads are issued
-constexpr uint32_t kColsT = 512, kColOT = 256;  // TMEM: S buffers [stream][2] of 64 columns, then O of each stream
+constexpr int kSBufs = 3;      // score buffers, tile i in i % 3
+// TMEM columns: S (and P over it), Q, O of each stream
+constexpr uint32_t kColsT = 512, kColQT = kSBufs * 64, kColOT = 256;
 
 template <int D>
 struct SmemT {
-  static constexpr int kRaw = D == 128 ? 5 : 8;
-  alignas(1024) uint8_t q[kRowsT * D * 2];
+  static constexpr int kRaw = D == 128 ? 4 : 8;
   alignas(1024) uint8_t k[kKStages][kTileT * D * 2];
   alignas(1024) uint8_t v[kVStages][kTileT * D * 2];
   alignas(1024) uint8_t raw[kRaw][2][kTileT * D];
@@ -57,7 +63,7 @@ struct SmemT {
   int flags[kScales];                   // bits 0-3: the 16-key groups that hold keys; bit 4: not every row sees every key; bit 5: a unit's first tile
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [stream][its tiles mod 2]
+  uint64_t s_full[kSBufs], p_full[kSBufs], o_done[kSBufs];
   uint64_t q_full, swap, drain[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -79,14 +85,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int n, bool mn) {
 // The issuing warps run converged and predicate the instruction itself on the
 // one lane `on`, so that the operands stay in uniform registers: inside a branch
 // on the lane each MMA took about 80 cycles to issue.
-__device__ __forceinline__ void mma_f16_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{.reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
 __device__ __forceinline__ void mma_f16_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
@@ -102,6 +100,36 @@ __device__ __forceinline__ void commit(uint32_t on, uint64_t* b) {
       "r"(on)
       : "memory");
 }
+// TMEM in MMA fragment order: of 16 rows and blocks of 8 columns, thread (g, c)
+// = (lane / 4, lane % 4) holds columns 2c, 2c + 1 of rows g and g + 8 (four
+// registers a block); packed to 16 bits, two registers.  A thread then meets a
+// quarter of a tile's keys in four rows instead of all keys in one, and reads a
+// quarter of the scales from shared memory.
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_half8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+constexpr uint32_t kLane16 = 16u << 16;  // rows 16-31 of a warp
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -114,27 +142,38 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One 64-key tile of raw codes -> FP16 in the MMA layout: 64-channel blocks of
-// [key][128 bytes].  Warp w of the converters takes the keys 8 w .. 8 w + 7.
+// [key][128 bytes].  Each warp w of the converters takes 16 keys.
 template <int D, int F>
 __device__ __forceinline__ void convert(uint32_t raw, uint32_t to, int w, int lane, bool clean) {
-  const int c = lane & 3, key = 8 * w + key_of(lane >> 2);
-  uint4 in[D / 64];
+  constexpr int KB = kTileT / (8 * kConvWarps);
+  const int c = lane & 3;
+  uint4 in[KB][D / 64];
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x) in[x] = lds128(raw + swizzled<D>(key, 4 * x + c));
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) in[kb][x] = lds128(raw + swizzled<D>(8 * (KB * w + kb) + key_of(lane >> 2), 4 * x + c));
   if (F == SAGE_CACHE_E4M3 && clean) {
 #pragma unroll
-    for (int x = 0; x < D / 64; ++x)
-      in[x] = make_uint4(no_nan<F>(in[x].x), no_nan<F>(in[x].y), no_nan<F>(in[x].z), no_nan<F>(in[x].w));
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        uint4& v = in[kb][x];
+        v = make_uint4(no_nan<F>(v.x), no_nan<F>(v.y), no_nan<F>(v.z), no_nan<F>(v.w));
+      }
   }
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x) {
-    uint32_t o[8];
-    const uint32_t iw[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+  for (int kb = 0; kb < KB; ++kb) {
+    const int key = 8 * (KB * w + kb) + key_of(lane >> 2);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) codes_to_f16<F>(iw[e], o[2 * e], o[2 * e + 1]);
-    const uint32_t row = to + x * (kTileT * 128) + key * 128;
-    sts128(row + (((2 * c) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
-    sts128(row + (((2 * c + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+    for (int x = 0; x < D / 64; ++x) {
+      uint32_t o[8];
+      const uint32_t iw[4] = {in[kb][x].x, in[kb][x].y, in[kb][x].z, in[kb][x].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) codes_to_f16<F>(iw[e], o[2 * e], o[2 * e + 1]);
+      const uint32_t row = to + x * (kTileT * 128) + key * 128;
+      sts128(row + (((2 * c) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
+      sts128(row + (((2 * c + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+    }
   }
 }
 
@@ -163,7 +202,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&sm.raw_full[s], 2);  // both producers
-      mbar_init(&sm.raw_empty[s], kConvWarps);
+      mbar_init(&sm.raw_empty[s], 2 * kConvWarps);
     }
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&sm.k_full[s], kConvWarps);
@@ -173,12 +212,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       mbar_init(&sm.v_full[s], kConvWarps);
       mbar_init(&sm.v_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      for (int k = 0; k < 2; ++k) {
-        mbar_init(&sm.s_full[s][k], 1);
-        mbar_init(&sm.p_full[s][k], 4);
-        mbar_init(&sm.o_done[s][k], 1);
-      }
+    for (int s = 0; s < kSBufs; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.o_done[s], 1);
     }
     mbar_init(&sm.q_full, 256);
     mbar_init(&sm.swap, 256);
@@ -198,9 +235,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1u, abort_flag, status, 100 + where, kDefaultWaitLimit));
   };
 
-  if (warp < kConv0) {
+  if (warp < kConvK) {
     // ------------------------------------------------------ softmax streams
-    const int sid = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int sid = warp >> 2, wrow = (warp & 3) * 32, row = wrow + lane, g = lane >> 2, c4 = lane & 3;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), col_o = lanes + kColOT + sid * D;
     float* vd = sm.vd[warp];
     uint32_t swaps = 0;
@@ -212,15 +249,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const int b = at.b, h = u.h, row0 = u.rt * kRowsT, ctx = at.s.ctx, cnt = at.s.cnt;
       const int rows = min(kRowsT, cnt * a.G - row0);
       const unsigned unit_end = u.start + at.s.n, seg_end = min(unit_end, st.e);
-      const int token = min((row0 + row) / a.G, a.T - 1);
       const bool idle = (warp & 3) * 32 >= rows;  // no row of this warp
 
-      // ---- this thread's half of its Q row: FP16, channels 0, 2, 1, 3 of each four, 128-byte swizzle
+      // ---- this thread's half of its Q row: FP16, channels 0, 2, 1, 3 of each four
       float f;
       {
         uint4 w[DH / 8];
         uint32_t top = 0;
-        const uint16_t* q = a.q + b * a.qb + token * a.qn + (h * a.G + (row0 + row) % a.G) * a.qh + sid * DH;
+        const uint16_t* q = a.q + b * a.qb + min((row0 + row) / a.G, a.T - 1) * a.qn + (h * a.G + (row0 + row) % a.G) * a.qh + sid * DH;
 #pragma unroll
         for (int x = 0; x < DH / 8; ++x) {
           w[x] = make_uint4(0, 0, 0, 0);
@@ -237,195 +273,228 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const int eq = q_exponent(top);
         const float down = __int_as_float((127 - eq) << 23);
         f = q_factor(a.sl2, eq);
-        const uint32_t qa = smem_u32(sm.q) + row * 128;
 #pragma unroll
-        for (int x = 0; x < DH / 8; ++x) {
-          const uint32_t ww[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-          uint32_t o[4];
+        for (int x0 = 0; x0 < DH / 8; x0 += 4) {
+          uint32_t o[16];
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            o[e] = pack_f16x2(__uint_as_float(ww[e] << 16) * down, __uint_as_float(ww[e + 1] << 16) * down);
-            o[e + 1] = pack_f16x2(__uint_as_float(ww[e] & 0xFFFF0000u) * down, __uint_as_float(ww[e + 1] & 0xFFFF0000u) * down);
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t ww[4] = {w[x0 + x].x, w[x0 + x].y, w[x0 + x].z, w[x0 + x].w};
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              o[4 * x + e] = pack_f16x2(__uint_as_float(ww[e] << 16) * down, __uint_as_float(ww[e + 1] << 16) * down);
+              o[4 * x + e + 1] =
+                  pack_f16x2(__uint_as_float(ww[e] & 0xFFFF0000u) * down, __uint_as_float(ww[e + 1] & 0xFFFF0000u) * down);
+            }
           }
-          const int ch = sid * (DH / 8) + x;  // 16-byte chunk of the row
-          sts128(qa + (ch >> 3) * (kRowsT * 128) + (((ch & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+          tmem_st16(lanes + kColQT + sid * (DH / 2) + 4 * x0, o);
         }
-        fence_async_smem();
+        tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&sm.q_full);
       }
-      const uint64_t f2 = pair(f, f);
-      float c = 0.0f;
-      bool none = true;  // nothing seen yet
-      uint64_t l0 = 0, l1 = 0;
-      int E = -126;
+      // From here on a thread works on its four fragment rows: row 8 r + g of the warp's 32, r = 0 .. 3.
+      float fr[4], c[4], l[4];
+      int E[4];
+      uint32_t none = 15;  // bit r: the row has seen nothing yet
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        fr[r] = __shfl_sync(0xffffffffu, f, g + 8 * r);
+        c[r] = l[r] = 0.0f;
+        E[r] = -126;
+      }
       bool fresh = true;  // no PV of this unit yet: the accumulator holds nothing
 
-      // one tile; first and later ones, seen whole by every row or masked
-      auto tile = [&](auto masked_tag, uint32_t cols, int slot, int k, uint64_t seen, int E_new) {
+      // Half `hv` of tile i's rows: the thread's rows 2 hv and 2 hv + 1.  `seen` (a masked tile): bit 16 q + 2 n + e: its
+      // row 2 hv + q sees key 8 n + 2 c4 + e.
+      auto half = [&](auto masked_tag, auto hv_tag, uint32_t cols, int i, uint32_t seen, int Ea, int Eb) {
         constexpr bool MASKED = decltype(masked_tag)::value;
-        const float* ks = sm.scale[slot][0];
-        const float* vs = MASKED ? sm.scale[slot][1] : sm.vd[slot];
-        const float down = __int_as_float((127 - E_new) << 23);
-        // c is raised until a row has seen something, with E, and where the sum of a tile's p passes 2^14 (so that FP16 holds each of
-        // them); the tile is then done again
-        bool raise = MASKED || __any_sync(0xffffffffu, none || E_new != E);
-        uint32_t p[32];
-        uint64_t s0, s1;
+        constexpr int hv = decltype(hv_tag)::value;
+        const int slot = i & (kScales - 1);
+        const float* ks = sm.scale[slot][0] + 2 * c4;
+        const float* vs = (MASKED ? sm.scale[slot][1] : sm.vd[slot]) + 2 * c4;
+        auto sees = [&](int q, int n, int e) { return !MASKED || ((seen >> (16 * q + 2 * n + e)) & 1u); };
+        const int E_new[2] = {Ea, Eb};
+        cols += hv * kLane16;
+        // c is raised until a row has seen something, with E, and where a thread's sum of a tile's p passes 2^14 (so that
+        // FP16 holds each of them); the half is then done again
+        bool raise = MASKED || __any_sync(0xffffffffu, ((none >> (2 * hv)) & 3u) || Ea != E[2 * hv]);
+        uint32_t p[16];
+        uint64_t sum[2];
         for (;;) {
-          uint32_t sa[16], sb[16];
+          uint32_t s[16];
           if (raise) {
-            float top = -INFINITY;
+            float top[2] = {-INFINITY, -INFINITY}, al_o[2];
 #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 16) {
-              tmem_ld16(cols + j0, sa);
-              tmem_wait_ld16(sa);
+            for (int cb = 0; cb < 2; ++cb) {
+              tmem_ld_frag4(cols + 32 * cb, s);
+              tmem_wait_ld16(s);
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 kk = *reinterpret_cast<const float4*>(ks + j0 + j);
-                const float x[4] = {__uint_as_float(sa[j]) * kk.x, __uint_as_float(sa[j + 1]) * kk.y,
-                                    __uint_as_float(sa[j + 2]) * kk.z, __uint_as_float(sa[j + 3]) * kk.w};
+              for (int m = 0; m < 4; ++m) {
+                const float2 kk = *reinterpret_cast<const float2*>(ks + 8 * (4 * cb + m));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (!MASKED || (seen >> (j0 + j + e)) & 1) top = fmaxf(top, x[e]);
+                  if (sees(e >> 1, 4 * cb + m, e & 1))
+                    top[e >> 1] = fmaxf(top[e >> 1], __uint_as_float(s[4 * m + e]) * ((e & 1) ? kk.y : kk.x));
               }
             }
-            const float c_new = none ? (top == -INFINITY ? 0.0f : top * f) : fmaxf(c, top * f);
-            const float al = none ? 0.0f : ex2(c - c_new), al_o = E_new == E ? al : al * ex2((float)(E - E_new));
-            none = none && top == -INFINITY;
-            c = c_new;
-            E = E_new;
-            l0 = mul2(l0, pair(al, al));
-            l1 = mul2(l1, pair(al, al));
-            if (!fresh && __any_sync(0xffffffffu, al_o != 1.0f)) {
-              // the PV before is done first, then the accumulator's row is multiplied
-              if (!(ok = wait(&sm.o_done[sid][(k - 1) & 1], (k - 1) >> 1, 3))) return;
+            bool moved = false;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int r = 2 * hv + q;
+              top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 1));
+              top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 2));
+              const bool nothing = (none >> r) & 1u;
+              const float c_new = nothing ? (top[q] == -INFINITY ? 0.0f : top[q] * fr[r]) : fmaxf(c[r], top[q] * fr[r]);
+              const float al = nothing ? 0.0f : ex2(c[r] - c_new);
+              al_o[q] = E_new[q] == E[r] ? al : al * ex2((float)(E[r] - E_new[q]));
+              moved |= al_o[q] != 1.0f;
+              if (top[q] != -INFINITY) none &= ~(1u << r);
+              c[r] = c_new;
+              E[r] = E_new[q];
+              l[r] *= al;
+            }
+            if (!fresh && __any_sync(0xffffffffu, moved)) {
+              // the stream's PV before is done first, then the accumulator's rows are multiplied
+              if (!(ok = wait(&sm.o_done[(i - 2) % kSBufs], (i - 2) / kSBufs, 3))) return;
               tc_fence_after();
 #pragma unroll 1
-              for (int x = 0; x < D; x += 16) {
-                tmem_ld16(col_o + x, sa);
-                tmem_wait_ld16(sa);
+              for (int x = 0; x < D; x += 32) {
+                tmem_ld_frag4(col_o + hv * kLane16 + x, s);
+                tmem_wait_ld16(s);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sa[e] = __float_as_uint(__uint_as_float(sa[e]) * al_o);
-                tmem_st16(col_o + x, sa);
+                for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * al_o[(e >> 1) & 1]);
+                tmem_st_frag4(col_o + hv * kLane16 + x, s);
               }
             }
           }
-          const uint64_t nc2 = pair(-c, -c);
-          s0 = s1 = 0;
-          // 16 keys from j0 on
-          auto chunk = [&](const uint32_t (&sr)[16], int j0) {
+          sum[0] = sum[1] = 0;
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 kk = *reinterpret_cast<const float4*>(ks + j0 + j);
-              float4 v = *reinterpret_cast<const float4*>(vs + j0 + j);
-              uint64_t x0 = mul2(pair(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), pair(kk.x, kk.y));
-              uint64_t x1 = mul2(pair(__uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3])), pair(kk.z, kk.w));
-              x0 = fma2(x0, f2, nc2);
-              x1 = fma2(x1, f2, nc2);
-              float2 a0 = unpair(x0), a1 = unpair(x1);
-              if (MASKED) {
-                const uint32_t on = (uint32_t)(seen >> (j0 + j));
-                if (!(on & 1)) { a0.x = -INFINITY; v.x = 0.0f; }
-                if (!(on & 2)) { a0.y = -INFINITY; v.y = 0.0f; }
-                if (!(on & 4)) { a1.x = -INFINITY; v.z = 0.0f; }
-                if (!(on & 8)) { a1.y = -INFINITY; v.w = 0.0f; }
-                v.x *= down; v.y *= down; v.z *= down; v.w *= down;
+          for (int cb = 0; cb < 2; ++cb) {
+            tmem_ld_frag4(cols + 32 * cb, s);
+            tmem_wait_ld16(s);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int n = 4 * cb + m;
+              const uint64_t kk = *reinterpret_cast<const uint64_t*>(ks + 8 * n), vv = *reinterpret_cast<const uint64_t*>(vs + 8 * n);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int r = 2 * hv + q;
+                const float2 x = unpair(mul2(pair(__uint_as_float(s[4 * m + 2 * q]), __uint_as_float(s[4 * m + 2 * q + 1])), kk));
+                float2 y = make_float2(fmaf(x.x, fr[r], -c[r]), fmaf(x.y, fr[r], -c[r]));
+                uint64_t v = vv;
+                if (MASKED) {
+                  const float2 vm = unpair(v);
+                  const float down = __int_as_float((127 - E[r]) << 23);
+                  if (!sees(q, n, 0)) y.x = -INFINITY;
+                  if (!sees(q, n, 1)) y.y = -INFINITY;
+                  v = pair(sees(q, n, 0) ? vm.x * down : 0.0f, sees(q, n, 1) ? vm.y * down : 0.0f);
+                }
+                const uint64_t w = pair(ex2(y.x), ex2(y.y));
+                sum[q] = add2(sum[q], w);
+                const float2 z = unpair(mul2(w, v));
+                p[2 * n + q] = pack_f16x2(z.x, z.y);
               }
-              const uint64_t p0 = pair(ex2(a0.x), ex2(a0.y)), p1 = pair(ex2(a1.x), ex2(a1.y));
-              s0 = add2(s0, p0);
-              s1 = add2(s1, p1);
-              const float2 w0 = unpair(mul2(p0, pair(v.x, v.y))), w1 = unpair(mul2(p1, pair(v.z, v.w)));
-              p[(j0 + j) / 2] = pack_f16x2(w0.x, w0.y);
-              p[(j0 + j) / 2 + 1] = pack_f16x2(w1.x, w1.y);
             }
-          };
-          tmem_ld16(cols, sa);
-          tmem_wait_ld16(sa);
-          tmem_ld16(cols + 16, sb);
-          chunk(sa, 0);
-          tmem_wait_ld16(sb);
-          tmem_ld16(cols + 32, sa);
-          chunk(sb, 16);
-          tmem_wait_ld16(sa);
-          tmem_ld16(cols + 48, sb);
-          chunk(sa, 32);
-          tmem_wait_ld16(sb);
-          chunk(sb, 48);
+          }
           if (raise) break;
-          const float2 y = unpair(add2(s0, s1));
-          raise = __any_sync(0xffffffffu, !(y.x + y.y <= 16384.0f));
+          const float2 y0 = unpair(sum[0]), y1 = unpair(sum[1]);
+          raise = __any_sync(0xffffffffu, !(y0.x + y0.y <= 16384.0f) || !(y1.x + y1.y <= 16384.0f));
           if (!raise) break;
         }
-        l0 = add2(l0, s0);
-        l1 = add2(l1, s1);
-        tmem_st16(cols, *reinterpret_cast<const uint32_t(*)[16]>(&p[0]));
-        tmem_st16(cols + 16, *reinterpret_cast<const uint32_t(*)[16]>(&p[16]));
-        tmem_wait_st();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float2 y = unpair(sum[q]);
+          l[2 * hv + q] += y.x + y.y;
+        }
+        tmem_st_half8(cols, p);
       };
 
       // ---- tiles of this stream
       int i = (int)(seg - st.s);
       i += (i & 1) ^ sid;
       for (; i < (int)(seg_end - st.s); i += 2) {
-        const int k = i >> 1, buf = k & 1, slot = i & (kScales - 1);
-        if (!(ok = wait(&sm.s_full[sid][buf], k >> 1, 2))) break;
+        const int buf = i % kSBufs, slot = i & (kScales - 1);
+        if (!(ok = wait(&sm.s_full[buf], i / kSBufs, 2))) break;
         tc_fence_after();
-        const uint32_t cols = lanes + (sid * 2 + buf) * 64;
+        const uint32_t cols = lanes + buf * 64;
         if (!idle) {
           const int flags = sm.flags[slot];
           if (!(flags & kMasked)) {
-            tile(std::false_type{}, cols, slot, k, ~0ull, sm.e[slot]);
+            const int E_new = sm.e[slot];
+            half(std::false_type{}, std::integral_constant<int, 0>{}, cols, i, ~0u, E_new, E_new);
+            if (ok) half(std::false_type{}, std::integral_constant<int, 1>{}, cols, i, ~0u, E_new, E_new);
           } else {
             const int64_t slot0 = (int64_t)(st.s + i - u.start) * kTileT;
             const int64_t d0 = slot0 - ctx;  // drafted token of the tile's first key (below 0: context)
-            uint64_t seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
-            if (row < rows && d0 < cnt && d0 > -64) {
-              const int lo = (int)max(d0, (int64_t)0), hi = min((int)(d0 + 64), cnt);  // drafted tokens [lo, hi)
-              uint64_t bits = 0;  // of tokens lo, lo + 1, ...
-              if (a.mask) {
-                const int words = (a.T + 31) / 32;
-                const uint32_t* m = a.mask + ((int64_t)b * a.T + token) * words;
-                for (int w = lo / 32; w <= (hi - 1) / 32; ++w) {
-                  const uint64_t word = __ldg(m + w);
-                  bits |= 32 * w >= lo ? word << (32 * w - lo) : word >> (lo - 32 * w);
-                }
-              } else if (token >= lo) {
-                bits = token - lo >= 63 ? ~0ull : (2ull << (token - lo)) - 1;
-              }
-              if (hi - lo < 64) bits &= (1ull << (hi - lo)) - 1;
-              seen |= bits << (lo - (int)d0);
-            }
+            uint32_t mine[2] = {0, 0};
+            int E_new[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (!((flags >> x) & 1)) seen &= ~(0xFFFFull << (16 * x));
-            float vm = 0.0f;
-            for (int j = 0; j < 64; ++j)
-              if ((seen >> j) & 1) vm = fmaxf(vm, sm.scale[slot][1][j]);
-            tile(std::true_type{}, cols, slot, k, seen, max(E, v_exponent(__float_as_uint(vm))));
+            for (int r = 0; r < 4; ++r) {
+              uint64_t seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
+              if (wrow + g + 8 * r < rows && d0 < cnt && d0 > -64) {
+                const int lo = (int)max(d0, (int64_t)0), hi = min((int)(d0 + 64), cnt);  // drafted tokens [lo, hi)
+                const int t = (row0 + wrow + g + 8 * r) / a.G;
+                uint64_t bits = 0;  // of tokens lo, lo + 1, ...
+                if (a.mask) {
+                  const int words = (a.T + 31) / 32;
+                  const uint32_t* m = a.mask + ((int64_t)b * a.T + t) * words;
+                  for (int w = lo / 32; w <= (hi - 1) / 32; ++w) {
+                    const uint64_t word = __ldg(m + w);
+                    bits |= 32 * w >= lo ? word << (32 * w - lo) : word >> (lo - 32 * w);
+                  }
+                } else if (t >= lo) {
+                  bits = t - lo >= 63 ? ~0ull : (2ull << (t - lo)) - 1;
+                }
+                if (hi - lo < 64) bits &= (1ull << (hi - lo)) - 1;
+                seen |= bits << (lo - (int)d0);
+              }
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (!((flags >> x) & 1)) seen &= ~(0xFFFFull << (16 * x));
+              float vm = 0.0f;
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                const uint32_t two = (uint32_t)(seen >> (8 * n + 2 * c4)) & 3u;
+                const float2 v = *reinterpret_cast<const float2*>(sm.scale[slot][1] + 8 * n + 2 * c4);
+                if (two & 1) vm = fmaxf(vm, v.x);
+                if (two & 2) vm = fmaxf(vm, v.y);
+                mine[r >> 1] |= two << (16 * (r & 1) + 2 * n);
+              }
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+              E_new[r] = max(E[r], v_exponent(__float_as_uint(vm)));
+            }
+            half(std::true_type{}, std::integral_constant<int, 0>{}, cols, i, mine[0], E_new[0], E_new[1]);
+            if (ok) half(std::true_type{}, std::integral_constant<int, 1>{}, cols, i, mine[1], E_new[2], E_new[3]);
           }
           if (!ok) break;
+          tmem_wait_st();
         }
         fresh = false;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[sid][buf]);
+        if (lane == 0) mbar_arrive(&sm.p_full[buf]);
       }
       if (!ok) break;
 
       // ---- the unit's end: wait for this stream's last PV, exchange the states, store half of the columns
       if (!fresh) {
-        const int last = ((int)(seg_end - st.s) - 1 - sid) >> 1;  // the stream's tile before the end
-        if (!(ok = wait(&sm.o_done[sid][last & 1], last >> 1, 4))) break;
+        int last = (int)(seg_end - st.s) - 1;  // the stream's last tile
+        last -= (last & 1) ^ sid;
+        if (!(ok = wait(&sm.o_done[last % kSBufs], last / kSBufs, 4))) break;
       }
-      float l;
-      {
-        const float2 x = unpair(l0), y = unpair(l1);
-        l = (x.x + x.y) + (y.x + y.y);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float x = l[r];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (c4 == 0) {
+          const int rw = wrow + g + 8 * r;
+          sm.l[sid][rw] = x;
+          sm.c[sid][rw] = (none >> r) & 1 ? -INFINITY : c[r];
+          sm.up[sid][rw] = fresh ? 0.0f : __int_as_float((127 + E[r]) << 23);  // 2^E; 0: the accumulator holds nothing
+        }
       }
-      sm.l[sid][row] = l;
-      sm.c[sid][row] = none ? -INFINITY : c;
-      sm.up[sid][row] = fresh ? 0.0f : __int_as_float((127 + E) << 23);  // 2^E; 0: the accumulator holds nothing
       tc_fence_before();
       mbar_arrive(&sm.swap);
       if (!(ok = wait(&sm.swap, swaps++, 5))) break;
@@ -433,10 +502,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       if (!idle) {
         const float ca = sm.c[0][row], cb = sm.c[1][row], cm = fmaxf(ca, cb);
         const float wa = ca == -INFINITY ? 0.0f : ex2(ca - cm), wb = cb == -INFINITY ? 0.0f : ex2(cb - cm);
-        l = sm.l[0][row] * wa + sm.l[1][row] * wb;
+        const float lt = sm.l[0][row] * wa + sm.l[1][row] * wb;
         const bool has_a = sm.up[0][row] != 0.0f, has_b = sm.up[1][row] != 0.0f;
         const bool whole = seg == u.start && seg_end == unit_end, on = row < rows;
-        const float inv = whole ? row_inverse(l) : 1.0f;
+        const float inv = whole ? row_inverse(lt) : 1.0f;
         const float fa = wa * sm.up[0][row] * inv, fb = wb * sm.up[1][row] * inv;
         const OutRow out(a, b, h, min(row0 + row, cnt * a.G - 1));
         float* part = part_of<kRowsT, D>(a, blockIdx.x, seg == u.start ? 1 : 0);
@@ -466,10 +535,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         }
         if (on && sid == 0) {
           if (whole) {
-            store_lse(a, b, h, row0 + row, cm, l);
+            store_lse(a, b, h, row0 + row, cm, lt);
           } else {
             part[kRowsT * D + row] = cm;
-            part[kRowsT * D + kRowsT + row] = l;
+            part[kRowsT * D + kRowsT + row] = lt;
           }
         }
       }
@@ -478,35 +547,36 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     }
   } else if (warp < kLoadK) {
     // ----------------------------------------------------------- converters
-    const int w = warp - kConv0;
+    // warps of K and of V, each at its own pace
+    const bool is_v = warp >= kConvV;
+    const int w = warp - (is_v ? kConvV : kConvK);
     int E = -126;  // of the tiles so far that every row sees whole
     for (int i = 0; i < n_tiles; ++i) {
       const int r = i % NR, slot = i & (kScales - 1);
       if (!wait(&sm.raw_full[r], i / NR, 6)) break;
       const int flags = sm.flags[slot];
-      const bool clean = flags & kMasked;
-      if (w == 0) {
-        if (flags & kFirst) E = -126;
-        if (!clean) {
-          const float v0 = sm.scale[slot][1][lane], v1 = sm.scale[slot][1][lane + 32];
-          E = max(E, v_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(v0, v1), 0.0f)))));
-          const float down = __int_as_float((127 - E) << 23);
-          sm.vd[slot][lane] = v0 * down;
-          sm.vd[slot][lane + 32] = v1 * down;
-          if (lane == 0) sm.e[slot] = E;
+      if (is_v) {
+        if (!wait(&sm.v_empty[i % kVStages], (i / kVStages) ^ 1, 8)) break;
+        convert<D, VF>(smem_u32(sm.raw[r][1]), smem_u32(sm.v[i % kVStages]), w, lane, flags & kMasked);
+      } else {
+        if (w == 0) {  // the softmax streams' V scales, seen behind k_full
+          if (flags & kFirst) E = -126;
+          if (!(flags & kMasked)) {
+            const float v0 = sm.scale[slot][1][lane], v1 = sm.scale[slot][1][lane + 32];
+            E = max(E, v_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(v0, v1), 0.0f)))));
+            const float down = __int_as_float((127 - E) << 23);
+            sm.vd[slot][lane] = v0 * down;
+            sm.vd[slot][lane + 32] = v1 * down;
+            if (lane == 0) sm.e[slot] = E;
+          }
         }
+        if (!wait(&sm.k_empty[i % kKStages], (i / kKStages) ^ 1, 7)) break;
+        convert<D, KF>(smem_u32(sm.raw[r][0]), smem_u32(sm.k[i % kKStages]), w, lane, false);
       }
-      if (!wait(&sm.k_empty[i % kKStages], (i / kKStages) ^ 1, 7)) break;
-      convert<D, KF>(smem_u32(sm.raw[r][0]), smem_u32(sm.k[i % kKStages]), w, lane, false);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[i % kKStages]);
-      if (!wait(&sm.v_empty[i % kVStages], (i / kVStages) ^ 1, 8)) break;
-      convert<D, VF>(smem_u32(sm.raw[r][1]), smem_u32(sm.v[i % kVStages]), w, lane, clean);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sm.v_full[i % kVStages]);
+        mbar_arrive(is_v ? &sm.v_full[i % kVStages] : &sm.k_full[i % kKStages]);
         mbar_arrive(&sm.raw_empty[r]);
       }
     }
@@ -563,8 +633,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     unsigned seg_end = st.s;  // of the unit that tile i belongs to
     int units = 0, begin = 0;
     for (int i = 0; i < n_tiles; ++i) {
-      const int s = i & 1, k = i >> 1;
-      const uint32_t sc = tmem + (s * 2 + (k & 1)) * 64;
+      const int buf = i % kSBufs;
+      const uint32_t sc = tmem + buf * 64;
       const bool next = st.s + i == seg_end;
       if (next) {
         go_to<kTileT, kRowsT>(a, at, st.s + i);
@@ -573,27 +643,26 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         begin = i;
       }
       if (warp == kQkWarpT) {
-        // a new unit's Q; S buffer k & 1 of the stream: PV of the tile two back in the stream has read its P
+        // a new unit's Q; the score buffer: PV of the tile three back has read its P
         if (next && !wait(&sm.q_full, units++, 13)) break;
-        if (k >= 2 && !wait(&sm.o_done[s][k & 1], (k >> 1) - 1, 14)) break;
+        if (i >= kSBufs && !wait(&sm.o_done[buf], i / kSBufs - 1, 14)) break;
         if (!wait(&sm.k_full[i % kKStages], i / kKStages, 15)) break;
         tc_fence_after();
-        const uint64_t qd = desc128(smem_u32(sm.q), 16, 1024), kd = desc128(smem_u32(sm.k[i % kKStages]), 16, 1024);
+        const uint64_t kd = desc128(smem_u32(sm.k[i % kKStages]), 16, 1024);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
-          mma_f16_ss(leader, sc, qd + (x / 4) * ((kRowsT * 128) >> 4) + 2 * (x % 4),
-                     kd + (x / 4) * (BLK >> 4) + 2 * (x % 4), idesc_f16(kTileT, false), x > 0);
-        commit(leader, &sm.s_full[s][k & 1]);
+          mma_f16_ts(leader, sc, tmem + kColQT + 8 * x, kd + (x / 4) * (BLK >> 4) + 2 * (x % 4), idesc_f16(kTileT, false), x > 0);
+        commit(leader, &sm.s_full[buf]);
         commit(leader, &sm.k_empty[i % kKStages]);
       } else {
-        if (!wait(&sm.v_full[i % kVStages], i / kVStages, 12) || !wait(&sm.p_full[s][k & 1], k >> 1, 11)) break;
+        if (!wait(&sm.v_full[i % kVStages], i / kVStages, 12) || !wait(&sm.p_full[buf], i / kSBufs, 11)) break;
         tc_fence_after();
         const uint64_t vd = desc128(smem_u32(sm.v[i % kVStages]), BLK, 1024);
-        const uint32_t o = tmem + kColOT + s * D, more = i >= begin + 2;  // the unit's first tile of a stream starts its O
+        const uint32_t o = tmem + kColOT + (i & 1) * D, more = i >= begin + 2;  // the unit's first tile of a stream starts its O
 #pragma unroll
         for (int x = 0; x < kTileT / 16; ++x)
           mma_f16_ts(leader, o, sc + 8 * x, vd + x * (2048 >> 4), idesc_f16(D, true), x > 0 ? 1u : more);
-        commit(leader, &sm.o_done[s][k & 1]);
+        commit(leader, &sm.o_done[buf]);
         commit(leader, &sm.v_empty[i % kVStages]);
       }
     }
