@@ -1,16 +1,19 @@
-"""Build the sm_100a shared library in-tree with nvcc (no GPU needed)."""
+"""Build the sm_100a shared library in-tree with nvcc (no GPU needed), and the
+CPython module of the serving calls with the host compiler."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsage_b200.so")
+SERVING = os.path.join(BUILD, "_sage_serving.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -49,6 +52,13 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
                                "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "serving_py.c")
+    if force or _stale(SERVING, [src, os.path.join(ROOT, "include", "sage_b200.h")]):
+        tmp = SERVING + f".tmp{os.getpid()}"
+        subprocess.check_call([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared",
+                               "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"), "-I",
+                               sysconfig.get_paths()["include"], src, "-o", tmp])
+        os.replace(tmp, SERVING)
     return LIB
 
 
