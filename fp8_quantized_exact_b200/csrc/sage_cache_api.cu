@@ -30,7 +30,7 @@ int check_cache(const sage_cache* c, int B, int N) {
 int check_table(const sage_cache* c, const int32_t* table, int table_pages, const int32_t* a, const int32_t* b,
                 void* ws, size_t ws_bytes, size_t need) {
   if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !table) return SAGE_ERR_INVALID_ARG;
-  if (table_pages < 1) return SAGE_ERR_INVALID_ARG;
+  if (table_pages < 1 || c->pages < 1) return SAGE_ERR_INVALID_ARG;
   if ((int64_t)table_pages * c->page_size > (1 << 28)) return SAGE_ERR_UNSUPPORTED;
   if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
       !aligned4(table) || !aligned4(a) || !aligned4(b))

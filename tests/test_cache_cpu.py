@@ -92,7 +92,7 @@ def cache_struct(**kw):
 
 CACHE_BAD = [(dict(k_codes=None), 1), (dict(v_scale=None), 1), (dict(k_codes=4100), 2), (dict(k_scale=4100), 2),
              (dict(k_format=2), 1), (dict(v_format=-1), 1), (dict(page_size=24), 2), (dict(page_size=256), 2),
-             (dict(page_size=8), 2), (dict(D=96), 2), (dict(pages=-1), 1), (dict(H=-1), 1),
+             (dict(page_size=8), 2), (dict(D=96), 2), (dict(pages=-1), 1), (dict(pages=0), 1), (dict(H=-1), 1),
              (dict(pages=1 << 20, H=2, page_size=128), 0), (dict(pages=1 << 23, H=2, page_size=128), 2)]
 
 

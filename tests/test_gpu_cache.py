@@ -276,6 +276,53 @@ def test_attn_trees(sage, ws, T, G, H, D, kf, vf):
         check_attn(q, cache, table, i32(*context), cnt, mask, out, lse)
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("D,kf,vf", [(128, E4M3, INT8), (128, INT8, INT8), (64, INT8, E4M3), (64, E4M3, E4M3)])
+@pytest.mark.parametrize("T,G", [(2, 4), (3, 3), (2, 8), (17, 1), (4, 8), (11, 3), (6, 8), (7, 7), (16, 8), (43, 3)])
+def test_attn_rows_per_head(sage, ws, T, G, D, kf, vf, page):
+    """8, 9, 16, 17, 32, 33, 48, 49, 128 and 129 rows per head: each side of every choice by rows."""
+    context = [0, 47, 64, 65, 230]
+    cache, table = filled(sage, [n + T for n in context], 2, page, D, kf, vf, seed=T)
+    r = gen(T + page)
+    mask = cu.tree_mask([[int(torch.randint(-1, i, (1,), generator=r)) if i else -1 for i in range(T)] for _ in context], DEV)
+    q = rand(len(context), T, 2 * G, D, seed=T + 1)
+    out, lse = run_attn(sage, ws, q, cache, table, i32(*context), None, mask)
+    assert status(sage, ws) == 0
+    check_attn(q, cache, table, i32(*context), None, mask, out, lse)
+
+
+@pytest.mark.parametrize("T,G,D", [(1, 2, 64), (3, 4, 128), (20, 4, 128)])
+def test_attn_many_sequences(sage, ws, T, G, D):
+    """More sequences than a warp counts at once, some without rows, of lengths from zero on."""
+    B = 75
+    context = [(7 * b * b) % 91 for b in range(B)]
+    count = [b % (T + 1) for b in range(B)]
+    cache, table = filled(sage, [n + T for n in context], 1, 16, D, INT8, E4M3, seed=T)
+    q = rand(B, T, G, D, seed=T)
+    out, lse = run_attn(sage, ws, q, cache, table, i32(*context), i32(*count), None)
+    assert status(sage, ws) == 0
+    check_attn(q, cache, table, i32(*context), i32(*count), None, out, lse)
+
+
+@pytest.mark.parametrize("T,G,D", [(64, 2, 128), (50, 1, 64)])
+def test_attn_many_rows_long(sage, ws, T, G, D):
+    """The variant for many rows over contexts that several CTAs share, scores that rise along the
+    context (so that offsets are raised often), and V scales that grow."""
+    context = [5000, 3, 1700]
+    cache, table = filled(sage, [n + T for n in context], 1, 64, D, INT8, E4M3, seed=T)
+    grow = torch.linspace(0.01, 6.0, 64, device=DEV)
+    for b, n in enumerate(context):
+        pages = table[b, :(n + T + 63) // 64].long()
+        for j, pg in enumerate(pages.tolist()):
+            cache[1][pg] *= float(0.05 + 3.0 * j / max(len(pages), 1))
+            cache[3][pg] *= grow * 2.0 ** (j % 9 - 4)
+    q = rand(3, T, G, D, seed=T) * 2
+    out, lse = run_attn(sage, ws, q, cache, table, i32(*context), None, None)
+    check_attn(q, cache, table, i32(*context), None, None, out, lse)
+    again, lse2 = run_attn(sage, ws, q, cache, table, i32(*context), None, None)
+    assert torch.equal(again, out) and torch.equal(lse2, lse) and status(sage, ws) == 0
+
+
 @pytest.mark.parametrize("T,G", [(1, 4), (8, 2), (40, 4)])
 def test_attn_empty_rows(sage, ws, T, G):
     """Rows whose mask leaves nothing (no context, no bits), whole empty
