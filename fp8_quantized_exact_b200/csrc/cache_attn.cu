@@ -148,6 +148,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
   auto row1_of = [&](int i) { return __shfl_sync(0xffffffffu, (i >> 5) == block ? ra1 : rb1, i & 31); };
   auto issue = [&](int i) {
     const int r0 = row0_of(i), r1 = row1_of(i), s = i % S;
+    if (i == a.stall_tile) return;  // test hook
     if (lane == 0 && (r0 >= 0 || r1 >= 0)) {
       uint64_t* bar = &sm.full[warp][s];
       tc::mbar_expect_tx(bar, (r0 >= 0 && r1 >= 0 ? 4 : 2) * kBox * D);
@@ -406,7 +407,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
       if (i + 1 < n_tiles) scales_of(i + 1, ks_next, vs_next);
       if ((r0 >= 0 || r1 >= 0) && i < issued) {
         if (!tc::wait_bounded(&sm.full[warp][s], (phase >> s) & 1u, &abort_flag, a.c.status, kWhereAttn,
-                              kDefaultWaitLimit, false))
+                              a.wait_limit, false))
           dead = true;
         phase ^= 1u << s;
         dead = __any_sync(0xffffffffu, dead);

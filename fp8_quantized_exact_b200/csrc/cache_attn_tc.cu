@@ -19,10 +19,15 @@
 //   warps 12-15      and of V: 128-byte swizzle that the MMAs read (V MN-major).
 //   warps 16, 17     TMA producers of raw K and V tiles (one box per page that the
 //                    tile touches) and of their scales (bulk copies).
-//   warps 18, 19     QK and PV issuers.  The A operands, Q and P, are in TMEM: what
-//                    bounds the kernel is shared-memory bandwidth (raw tile in and
-//                    out, FP16 tile in and out: 112 KB per tile at D = 128, about 900
-//                    cycles; with Q in shared memory it was 144 KB).
+//   warps 18, 19     QK and PV issuers; the A operands, Q and P, are in TMEM.
+// What bounds it: the instructions and waits of the roles, not a pipe.  A tile of 64
+// keys takes about 1,900 cycles on an SM at 128 rows (tensor pipe 26% busy, issue
+// slots 46%) and little less at 16 rows; an M = 128 MMA costs its issuer about 65
+// cycles for any N up to 128.  Tried and not kept, as factors of the time of 64 drafted
+// tokens over 4 contexts of 20000..37810 (424 us): pairs of tiles per QK MMA 1.27, P in
+// columns of its own with Q in shared memory 1.05, one QK issuer per stream 1.25,
+// both score loads of a half before one wait 1.12, two converter warps per side
+// instead of four 1.22, 32x32b loads with every scale read by every thread 1.15.
 // Channels are in the order 0, 2, 1, 3 within each four, in Q, K and V alike, as the
 // conversion yields them; the output undoes it.
 //
@@ -232,7 +237,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   const int n_tiles = (int)(st.e - st.s);
   // the phase of number `phase` of a barrier, by a whole warp
   auto wait = [&](uint64_t* bar, uint32_t phase, int where) -> bool {
-    return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1u, abort_flag, status, 100 + where, kDefaultWaitLimit));
+    return __all_sync(0xffffffffu, wait_bounded(bar, phase & 1u, abort_flag, status, 100 + where, a.wait_limit));
   };
 
   if (warp < kConvK) {
@@ -613,6 +618,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const uint32_t valid = __ballot_sync(0xffffffffu, lane < 4 && row >= 0);
       const uint32_t boxes = __ballot_sync(0xffffffffu, lane < 4 && row >= 0 && lane % per == 0);
       if (!wait(&sm.raw_empty[r], (i / NR) ^ 1, 9)) break;
+      if (i == a.stall_tile) break;  // test hook: nothing comes from here on
       if (lane == 0) {
         if (side == 0) sm.flags[slot] = (int)valid | (masked || valid != 15u ? kMasked : 0) | (begins ? kFirst : 0);
         mbar_expect_tx(&sm.raw_full[r], __popc(boxes) * box * (D + 4));
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       issued = i + 1;
     }
     for (int i = max(0, issued - NR); i < issued; ++i)
-      wait_bounded(&sm.raw_full[i % NR], (uint32_t)((i / NR) & 1), abort_flag, nullptr, 110, kDefaultWaitLimit, false);
+      wait_bounded(&sm.raw_full[i % NR], (uint32_t)((i / NR) & 1), abort_flag, nullptr, 110, a.wait_limit, false);
   } else {
     // -------------------------------------------------------------- issuers
     const uint32_t leader = lane == 0;
@@ -669,7 +675,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     __syncwarp();
     uint64_t* drain = &sm.drain[warp - kQkWarpT];
     commit(leader, drain);
-    wait_bounded(drain, 0, abort_flag, nullptr, 116, kDefaultWaitLimit, false);
+    wait_bounded(drain, 0, abort_flag, nullptr, 116, a.wait_limit, false);
   }
 
   tc_fence_before();

@@ -88,6 +88,8 @@ struct CacheAttnArgs {
   int B, T, Hq, G;         // G = Hq / H
   float sl2;               // fl32(sm_scale * log2 e)
   void* workspace;
+  long long wait_limit;    // clock cycles a bounded device wait may spin
+  int stall_tile;          // test hook: the producers withhold this tile of their own counting (-1: none)
 };
 size_t cache_attn_workspace_bytes();
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s);

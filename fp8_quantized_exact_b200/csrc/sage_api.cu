@@ -256,6 +256,11 @@ std::vector<int> host_chunks(int H, int hc) {
 }
 }  // namespace
 
+namespace sage {
+long long debug_wait_limit() { return g_wait_limit.load(); }
+int debug_stall_tile() { return g_stall_tile.load(); }
+}  // namespace sage
+
 extern "C" {
 
 int sage_workspace_bytes(int op, int B, int N, int H, int D, size_t* bytes) {

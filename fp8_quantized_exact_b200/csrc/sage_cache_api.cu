@@ -213,6 +213,8 @@ int sage_cache_attn(sage_view_bf16 q, const sage_cache* cache, const int32_t* pa
   a.B = B; a.T = T; a.Hq = Hq; a.G = Hq / cache->H;
   a.sl2 = log2_scale(sm_scale, cache->D);
   a.workspace = at<void>(workspace, align_up(SAGE_STATUS_BYTES));
+  a.wait_limit = debug_wait_limit();
+  a.stall_tile = debug_stall_tile();
   return launch_cache_attn(a, static_cast<cudaStream_t>(stream));
 }
 

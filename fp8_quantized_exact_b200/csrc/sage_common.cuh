@@ -106,6 +106,9 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t& r0, uint32_
 
 // Host-side launchers (defined in the .cu files).
 namespace sage {
+// What sage_debug_set_stall set: a wait limit in clock cycles and a withheld tile (-1: none).
+long long debug_wait_limit();
+int debug_stall_tile();
 // Outputs and scratch of the single-launch prepass (device pointers).
 struct FusedOut {
   int8_t* q8;

@@ -317,7 +317,8 @@ SAGE_API int sage_get_mainloop(void);
  * cycles (<= 0: the default, about one second).  In the single-launch
  * prepass (sage_quant_qkv, and sage_attn_fwd where it uses it) the first K
  * statistics tile of head unit b*H + h == k_tile is never counted in
- * instead (wait site 45).  A withheld tile makes the
+ * instead (wait site 45).  In sage_cache_attn each producer stops before the
+ * tile of that number of its own counting.  A withheld tile makes the
  * waits run out: the kernel records SAGE_ERR_TIMEOUT in the status word,
  * abandons the work, frees its tensor memory and returns, leaving the
  * context usable.  Process-wide; call with (-1, 0) to restore. */

@@ -534,6 +534,25 @@ def test_attn_streams_and_graphs(sage, T, G):
     assert sage.sage_read_device_status(w) == 0
 
 
+@pytest.mark.parametrize("T,G", [(1, 4), (16, 8)])
+def test_attn_withheld_tile_times_out_and_context_survives(sage, ws, T, G):
+    """Producers that withhold their first tile: the bounded waits behind it run out (about 1 ms each), the
+    status word says so, the kernel returns, and the next call is right."""
+    context = [20000]
+    cache, table = filled(sage, [20000 + T], 2, 64, 128, INT8, E4M3, seed=50)
+    q = rand(1, T, 2 * G, 128, seed=51)
+    try:
+        sage.sage_debug_set_stall(0, 2_000_000)
+        run_attn(sage, ws, q, cache, table, i32(*context), None, None)
+        assert status(sage, ws) == sage.SAGE_ERR_TIMEOUT
+    finally:
+        sage.sage_debug_set_stall(-1, 0)
+    sage.sage_clear_device_status(ws)
+    out, lse = run_attn(sage, ws, q, cache, table, i32(*context), None, None)
+    assert status(sage, ws) == 0
+    check_attn(q, cache, table, i32(*context), None, None, out, lse)
+
+
 def test_step_together(sage, ws):
     """A serving loop: prompts rotated and appended, single-token steps, then a
     drafted tree over the cache, against FP64 attention on the dequantised rows, captured as a graph."""
