@@ -56,14 +56,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Launch shape by the number of 8-row groups.  The registers leave room for a
-// block of the joining kernel beside the CTA.
+// Launch shape by D and the number of 8-row groups.  A tile of D = 64 is half the work between the same waits, so more
+// warps run beside each other: 12 are three for each quarter of the SM, which 168 registers allow.  Measured on B200
+// (us, D = 64; one context of 151241 at 4 rows per head, 16 contexts of 500..16384 at 16 and 48): 10, 12, 14, 16, 20
+// warps 49.4, 44.4, 47.3, 46.4, 74.7 at 4 rows; 8 and 12 warps 71 and 66 at 16 rows, 159 and 142 at 48.  D = 128 at 4 rows
+// (64 contexts of 1..8192): 8, 10, 11 warps 127, 122, 125; shared memory ends there.
 template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 1 ? 10 : 8;
+  static constexpr int kWarps = D == 64 ? 12 : NT == 1 ? 10 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRegs = NT == 1 ? 168 : 224;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRegs = D == 64 ? (NT == 1 ? 144 : 168) : NT == 1 ? 168 : 224;
+  static constexpr int kStages = D == 64 ? 3 : 2;
   static_assert(kStages * kTile * D >= 8 * NT * D * 4, "a part fits a warp's ring of K");
 };
 

@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     // ------------------------------------------------------ softmax streams
     const int sid = warp >> 2, wrow = (warp & 3) * 32, row = wrow + lane, g = lane >> 2, c4 = lane & 3;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), col_o = lanes + kColOT + sid * D;
-    float* vd = sm.vd[warp];
     uint32_t swaps = 0;
     bool ok = true;
     Place at = place_of<kTileT, kRowsT>(a, st.s);
