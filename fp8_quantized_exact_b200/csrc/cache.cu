@@ -83,15 +83,16 @@ __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const Appen
   constexpr int CH = D / (8 * kLanes);  // chunks of 8 values of a thread: 8 (lane + 4 j) ..
   const int b = blockIdx.y, lane = threadIdx.x % kLanes;
   const int64_t r0 = (int64_t)blockIdx.x * (kPerBlock * ROWS) + threadIdx.x / kLanes;
+  begin_dependent();
   int count = a.N;
   if (a.count) {
-    count = __ldg(a.count + b);
+    count = a.count[b];
     if ((count < 0 || count > a.N) && r0 == 0 && lane == 0) flag_bad(a.c.status, kWhereAppend);
     count = max(min(count, a.N), 0);
   }
   const int64_t rows = (((int64_t)count + (1 << gs) - 1) >> gs << gs) * a.c.H;
   if ((int64_t)blockIdx.x * (kPerBlock * ROWS) >= rows) return;
-  const int64_t start = a.start ? __ldg(a.start + b) : 0;
+  const int64_t start = a.start ? a.start[b] : 0;
   uint4 u[2][ROWS][CH];
   int64_t row[ROWS];
 #pragma unroll
@@ -104,8 +105,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const Appen
       for (int j = 0; j < CH; ++j) {
         u[i][k][j] = make_uint4(0, 0, 0, 0);
         if (on)
-          u[i][k][j] = __ldg(reinterpret_cast<const uint4*>(a.x[i] + b * a.sb[i] + t.n * a.sn[i] + t.h * a.sh[i] +
-                                                            8 * (lane + kLanes * j)));
+          u[i][k][j] = *reinterpret_cast<const uint4*>(a.x[i] + b * a.sb[i] + t.n * a.sn[i] + t.h * a.sh[i] +
+                                                       8 * (lane + kLanes * j));
       }
     row[k] = on ? cache_row(a.c, b, t.h, start + t.n) : -1;
     if (on && row[k] < 0 && lane == 0) flag_bad(a.c.status, kWhereAppend);
@@ -184,15 +185,16 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArg
   constexpr int CH = D / (8 * kLanes);
   const int b = blockIdx.y, lane = threadIdx.x % kLanes;
   const int64_t r0 = (int64_t)blockIdx.x * (kPerBlock * ROWS) + threadIdx.x / kLanes;
+  begin_dependent();
   int count = a.N;
   if (a.count) {
-    count = __ldg(a.count + b);
+    count = a.count[b];
     if ((count < 0 || count > a.N) && r0 == 0 && lane == 0) flag_bad(a.c.status, kWhereRead);
     count = max(min(count, a.N), 0);
   }
   const int64_t rows = (((int64_t)count + (1 << gs) - 1) >> gs << gs) * a.c.H;
   if (r0 >= rows) return;
-  const int64_t start = a.start ? __ldg(a.start + b) : 0;
+  const int64_t start = a.start ? a.start[b] : 0;
   uint2 w[2][ROWS][CH];
   float scale[2][ROWS];
   int64_t row[ROWS];
@@ -213,8 +215,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const ReadArg
       if (row[k] >= 0 && a.y[i]) {
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-          w[i][k][j] = __ldg(reinterpret_cast<const uint2*>(a.c.codes[i] + row[k] * D + 8 * (lane + kLanes * j)));
-        scale[i][k] = __ldg(a.c.scale[i] + row[k]);
+          w[i][k][j] = *reinterpret_cast<const uint2*>(a.c.codes[i] + row[k] * D + 8 * (lane + kLanes * j));
+        scale[i][k] = a.c.scale[i][row[k]];
       }
 #pragma unroll
   for (int k = 0; k < ROWS; ++k)
@@ -245,20 +247,18 @@ dim3 rows_grid(int N, int H, int per_block, int B) {
 
 int launch_cache_append(const AppendArgs& a, cudaStream_t s) {
   const int gs = group_shift(a.N);
-  if (a.c.D == 128)
-    cache_append_kernel<128, 1><<<rows_grid(a.N, a.c.H, kPerBlock, a.B), kCacheThreads, 0, s>>>(a, gs);
-  else
-    cache_append_kernel<64, 2><<<rows_grid(a.N, a.c.H, 2 * kPerBlock, a.B), kCacheThreads, 0, s>>>(a, gs);
-  return cudaGetLastError() == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+  return a.c.D == 128 ? launch_dependent(cache_append_kernel<128, 1>, rows_grid(a.N, a.c.H, kPerBlock, a.B),
+                                         kCacheThreads, 0, s, a, gs)
+                      : launch_dependent(cache_append_kernel<64, 2>, rows_grid(a.N, a.c.H, 2 * kPerBlock, a.B),
+                                         kCacheThreads, 0, s, a, gs);
 }
 
 int launch_cache_read(const ReadArgs& a, cudaStream_t s) {
   const int gs = group_shift(a.N);
-  if (a.c.D == 128)
-    cache_read_kernel<128, 1><<<rows_grid(a.N, a.c.H, kPerBlock, a.B), kCacheThreads, 0, s>>>(a, gs);
-  else
-    cache_read_kernel<64, 2><<<rows_grid(a.N, a.c.H, 2 * kPerBlock, a.B), kCacheThreads, 0, s>>>(a, gs);
-  return cudaGetLastError() == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+  return a.c.D == 128 ? launch_dependent(cache_read_kernel<128, 1>, rows_grid(a.N, a.c.H, kPerBlock, a.B),
+                                         kCacheThreads, 0, s, a, gs)
+                      : launch_dependent(cache_read_kernel<64, 2>, rows_grid(a.N, a.c.H, 2 * kPerBlock, a.B),
+                                         kCacheThreads, 0, s, a, gs);
 }
 
 }  // namespace sage

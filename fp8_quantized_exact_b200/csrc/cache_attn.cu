@@ -106,7 +106,14 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
   Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) tc::mbar_init(&sm.full[warp][s], 1);
+    sm.cut[warp].slot = -1;
+    if (warp == 0) sm.cut[W].slot = -1;
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
+  begin_dependent_tma();
   const Stretch st = find_stretch<kTile, R, W>(a, blockIdx.x, gridDim.x);
   if (blockIdx.x == 0)  // lengths that cannot be
     for (int b = threadIdx.x; b < a.B; b += Sh::kThreads) {
@@ -116,18 +123,11 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
         flag_bad(a.c.status, kWhereAttn);
     }
   if (st.s >= st.e) return;
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) tc::mbar_init(&sm.full[warp][s], 1);
-    sm.cut[warp].slot = -1;
-    if (warp == 0) sm.cut[W].slot = -1;
-  }
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  __syncwarp();
 
   // ---- this warp's tiles: list indices [first, last)
   const unsigned share = st.share / W, first = min(st.s + warp * share, st.e), last = min(first + share, st.e);
   const int n_tiles = (int)(last - first);
-  const Place begin = n_tiles > 0 ? place_of<kTile, R>(a, first) : Place{};
+  const Place begin = n_tiles > 0 ? place_of<kTile, R>(a, st.own, first) : Place{};
   // cache rows of the two boxes of tiles 32 blk + lane, -1 for a box without keys: this block of 32 tiles and the next
   Place walk = begin;
   auto rows_of_block = [&](int blk, int& r0, int& r1) {
@@ -168,8 +168,8 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
   // the scales of the tile's key `lane`
   auto scales_of = [&](int i, float& ks, float& vs) {
     const int r0 = row0_of(i), r1 = row1_of(i), row = lane < kBox ? r0 : r1;
-    ks = row < 0 ? 0.0f : __ldg(a.c.scale[0] + row + (lane & 15));
-    vs = row < 0 ? 0.0f : __ldg(a.c.scale[1] + row + (lane & 15));
+    ks = row < 0 ? 0.0f : a.c.scale[0][row + (lane & 15)];
+    vs = row < 0 ? 0.0f : a.c.scale[1][row + (lane & 15)];
   };
   int issued = min(S, n_tiles);
   for (int i = 0; i < issued; ++i) issue(i);
@@ -209,7 +209,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (lr < rows) v = __ldg(reinterpret_cast<const uint4*>(q + 64 * x + 8 * y));
+          if (lr < rows) v = *reinterpret_cast<const uint4*>(q + 64 * x + 8 * y);
           const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -227,7 +227,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
         put(s, make_uint2(pack_f16x2(__uint_as_float(w0 << 16) * down, __uint_as_float(w1 << 16) * down),
                           pack_f16x2(__uint_as_float(w0 & 0xFFFF0000u) * down, __uint_as_float(w1 & 0xFFFF0000u) * down)));
       }
-      return q_factor(a.sl2, eq);
+      return q_factor(eq);
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -299,23 +299,40 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
       uint32_t seen = 0xFFFFFFFFu;  // bit (nt * 8 + hf * 4 + j * 2 + e)
       if (MASKED) {
         seen = 0;
+        const int64_t d0 = slot0 - ctx;  // drafted token of the tile's first key (below 0: context)
+        const bool drafts = d0 < cnt && d0 > -kTile;
+        const int lo = (int)max(d0, (int64_t)0), hi = drafts ? min((int)(d0 + kTile), cnt) : lo;  // drafted tokens [lo, hi)
+        const int words = (a.T + 31) / 32, w0 = lo / 32;
+        uint32_t m[NT][2][2];  // the rows' mask words of lo and behind, all loads before the first use
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int lr = 8 * nt + 2 * c4 + e, t = (row0 + lr) / a.G;
 #pragma unroll
+            for (int w = 0; w < 2; ++w)
+              m[nt][e][w] = a.mask && drafts && lr < rows && w0 + w < words
+                                ? a.mask[((int64_t)b * a.T + t) * words + w0 + w] : 0u;
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * nt + 2 * c4 + e, t = (row0 + lr) / a.G;
+            uint32_t bits = d0 <= -kTile ? ~0u : d0 >= 0 ? 0u : ~0u >> (int)(kTile + d0);  // the tile's keys
+            if (drafts && lr < rows) {
+              uint32_t draft = a.mask ? __funnelshift_r(m[nt][e][0], m[nt][e][1], lo)
+                                      : t < lo ? 0u : t - lo >= 31 ? ~0u : (2u << (t - lo)) - 1;
+              if (hi - lo < 32) draft &= (1u << (hi - lo)) - 1;
+              bits |= draft << (int)(lo - d0);
+            }
+            if (!box0) bits &= 0xFFFF0000u;
+            if (!box1) bits &= 0x0000FFFFu;
+#pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const int64_t slot = slot0 + 16 * hf + 8 * j + key_of(g);
-                bool on = slot < ctx;
-                if (!on && slot < (int64_t)ctx + cnt && lr < rows) {
-                  const int d = (int)(slot - ctx);
-                  on = a.mask ? (__ldg(a.mask + ((int64_t)b * a.T + t) * ((a.T + 31) / 32) + d / 32) >> (d % 32)) & 1u
-                              : d <= t;
-                }
-                if (on && (hf ? box1 : box0)) seen |= 1u << (nt * 8 + hf * 4 + j * 2 + e);
+                if ((bits >> (16 * hf + 8 * j + key_of(g))) & 1u) seen |= 1u << (nt * 8 + hf * 4 + j * 2 + e);
                 else s[hf][nt][2 * j + e] = -INFINITY;
               }
           }
@@ -351,7 +368,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
             const bool none = rs[nt].thr[e] == -INFINITY;
             const float c = none ? (top == -INFINITY ? 0.0f : top * fe) : fmaxf(c_old, top * fe);
             al_l[e] = none ? 0.0f : ex2f(c_old - c);
-            if (top != -INFINITY && (none || c > c_old)) rs[nt].thr[e] = top + kRaise / fe;
+            if (top != -INFINITY && (none || c > c_old)) rs[nt].thr[e] = __fadd_rd(top, kRaise / fe);
             const float d_old = e ? dn_old.y : dn_old.x;
             const int E_old = 127 - (__float_as_int(d_old) >> 23);
             const int E = min(max(E_old, (__float_as_int(vm) >> 23) - 126), 126);
@@ -406,7 +423,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
 
     for (; i < i_end; ++i) {
       const int r0 = row0_of(i), r1 = row1_of(i), s = i % S;
-      const float ks = ks_next, vs = vs_next;
+      const float ks = ks_next * a.sl2, vs = vs_next;  // multiplied here: at the load it would wait for it
       if (i + 1 < n_tiles) scales_of(i + 1, ks_next, vs_next);
       if ((r0 >= 0 || r1 >= 0) && i < issued) {
         if (!tc::wait_bounded(&sm.full[warp][s], (phase >> s) & 1u, &abort_flag, a.c.status, kWhereAttn,
@@ -530,8 +547,7 @@ int launch_mma(const CacheAttnArgs& a, cudaStream_t s) {
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SAGE_ERR_CUDA;
-  fn<<<kMaxCtas, Sh::kThreads, smem, s>>>(mk, mv, a);
-  if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
+  if (const int rc = launch_dependent(fn, dim3(kMaxCtas), Sh::kThreads, smem, s, mk, mv, a)) return rc;
   return launch_join<kTile, 8 * NT, D, Sh::kWarps>(a, s);
 }
 
@@ -555,7 +571,7 @@ size_t cache_attn_workspace_bytes() { return kPartBytes; }
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   // The tcgen05 variant takes 128 rows at once at nearly the time of 16; this one reads and converts the cache again for
   // each 16.  Measured on B200 (us here against there, cold L2, 16 sequences of 500..16384, 8 heads): D = 128: 16 rows
-  // 104 / 169, 32 rows 167 / 175, 40 rows 220 / 181, 128 rows 544 / 218; D = 64: 32 rows 118 / 153, 48 rows 151 / 155,
+  // 104 / 169, 32 rows 167 / 175, 40 rows 220 / 181, 128 rows 544 / 218; D = 64: 32 rows 118 / 153, 48 rows 142 / 155,
   // 56 rows 187 / 157.
   if (a.T * a.G > (a.c.D == 128 ? 32 : 48)) return launch_cache_attn_tc(a, s);
   return a.c.D == 128 ? by_rows<128>(a, s) : by_rows<64>(a, s);

@@ -26,8 +26,8 @@ struct Seq {
 template <int TILE, int R>
 __device__ __forceinline__ Seq seq_of(const CacheAttnArgs& a, int b) {
   Seq s;
-  s.ctx = max(__ldg(a.context + b), 0);
-  s.cnt = a.count ? min(max(__ldg(a.count + b), 0), a.T) : a.T;
+  s.ctx = max(a.context[b], 0);
+  s.cnt = a.count ? min(max(a.count[b], 0), a.T) : a.T;
   const unsigned cap = (unsigned)a.c.table_pages << a.c.page_shift;
   s.n = (min((unsigned)s.ctx + (unsigned)s.cnt, cap) + TILE - 1) / TILE;
   s.rt = (s.cnt * a.G + R - 1) / R;
@@ -68,13 +68,18 @@ __device__ __forceinline__ Unit unit_of(const Place& p, unsigned idx) {
 // barrier.  STEP: stretches are multiples of it.
 struct Stretch {
   unsigned s, e, share, total;
+  Seq own;  // sequence `lane`, for place_of (a second load would be another trip to L2)
 };
 template <int TILE, int R, int STEP>
 __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
-  unsigned sum = 0;
-  for (int b = lane; b < a.B; b += 32) sum += seq_of<TILE, R>(a, b).per;
   Stretch t;
+  t.own.ctx = t.own.cnt = 0;
+  t.own.n = t.own.rt = 1;
+  t.own.per = 0;
+  if (lane < a.B) t.own = seq_of<TILE, R>(a, lane);
+  unsigned sum = t.own.per;
+  for (int b = lane + 32; b < a.B; b += 32) sum += seq_of<TILE, R>(a, b).per;
   t.total = __reduce_add_sync(0xffffffffu, sum);
   t.share = max((t.total + ctas * STEP - 1) / (ctas * STEP), 1u) * STEP;
   t.s = min((unsigned)cta * t.share, t.total);
@@ -82,17 +87,17 @@ __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta,
   return t;
 }
 template <int TILE, int R>
-__device__ __forceinline__ Place place_of(const CacheAttnArgs& a, unsigned idx) {
+__device__ __forceinline__ Place place_of(const CacheAttnArgs& a, const Seq& own, unsigned idx) {
   const int lane = threadIdx.x & 31;
   Place p;
   p.base = 0;
   p.b = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    Seq s;
-    s.ctx = s.cnt = 0;
-    s.n = s.rt = 1;
-    s.per = 0;
-    if (b0 + lane < a.B) s = seq_of<TILE, R>(a, b0 + lane);
+    Seq s = own;
+    if (b0 > 0) {
+      s.per = 0;
+      if (b0 + lane < a.B) s = seq_of<TILE, R>(a, b0 + lane);
+    }
     unsigned incl = s.per;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -121,6 +126,12 @@ template <int TILE, int R>
 inline bool list_fits(const CacheAttnArgs& a) {
   const double n = (((double)a.c.table_pages * (1 << a.c.page_shift)) + TILE - 1) / TILE;
   return n * a.B * a.c.H * ((a.T * a.G + R - 1) / R) < 2147483648.0;
+}
+
+// begin_dependent, also for codes that a kernel before wrote by ordinary stores and TMA reads.
+__device__ __forceinline__ void begin_dependent_tma() {
+  begin_dependent();
+  asm volatile("fence.proxy.async;" ::: "memory");
 }
 
 constexpr int kMaxCtas = 148;  // one per SM
@@ -165,24 +176,24 @@ __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, int b, int h, 
 
 // Joins the parts of the unit that begins in CTA blockIdx.x's stretch and is
 // cut by its end; blockIdx.y of gridDim.y takes a share of the rows.  The
-// blocks become resident beside the CTAs of the main kernel, find their unit
-// and wait for them.
+// blocks find their unit while the CTAs of the main kernel end, and wait for them.
 constexpr int kJoinThreads = 128;
 template <int TILE, int R, int D, int STEP>
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const CacheAttnArgs a, int ctas) {
   constexpr int RB = 8;  // rows at a time
   __shared__ float c_s[RB][kMaxCtas], l_s[RB][kMaxCtas];  // offsets, then weights; denominators
   __shared__ float c_row[RB], l_row[RB];
+  // the lengths are older than the kernel in front, which waited for them
   const Stretch st = find_stretch<TILE, R, STEP>(a, blockIdx.x, ctas);
   Place p;
   Unit u;
   unsigned end = 0;
   if (st.s < st.e) {
-    p = place_of<TILE, R>(a, st.e - 1);
+    p = place_of<TILE, R>(a, st.own, st.e - 1);
     u = unit_of(p, st.e - 1);
     end = u.start + p.s.n;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // from here on the parts are written
+  begin_dependent();
   if (st.s >= st.e || u.start < st.s || end <= st.e) return;
   const int first = blockIdx.x, np = (int)((end - 1) / st.share) - first + 1;
   const int rows = min(R, p.s.cnt * a.G - u.rt * R);
@@ -233,20 +244,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const Cac
   }
 }
 
-// Behind the main kernel on its stream, as its programmatic dependent.
 template <int TILE, int R, int D, int STEP>
 int launch_join(const CacheAttnArgs& a, cudaStream_t s) {
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kMaxCtas, R >= 64 ? 4 : 1);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<TILE, R, D, STEP>, a, kMaxCtas) == cudaSuccess ? SAGE_OK
-                                                                                                       : SAGE_ERR_CUDA;
+  return launch_dependent(cache_attn_join_kernel<TILE, R, D, STEP>, dim3(kMaxCtas, R >= 64 ? 4 : 1), kJoinThreads, 0, s, a,
+                          kMaxCtas);
 }
 
 }  // namespace cattn

@@ -193,17 +193,6 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   volatile int* abort_flag = &sm.abort_flag;
   DeviceStatus* status = a.c.status;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Stretch st = find_stretch<kTileT, kRowsT, 1>(a, blockIdx.x, gridDim.x);
-  if (blockIdx.x == 0)  // lengths that cannot be
-    for (int b = threadIdx.x; b < a.B; b += kThreadsT) {
-      const int ctx = a.context[b], cnt = a.count ? a.count[b] : a.T;
-      if (ctx < 0 || cnt < 0 || cnt > a.T ||
-          (long long)ctx + cnt > ((long long)a.c.table_pages << a.c.page_shift))
-        flag_bad(status, kWhereAttn);
-    }
-  if (st.s >= st.e) return;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&sm.raw_full[s], 2);  // both producers
@@ -229,6 +218,16 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  begin_dependent_tma();
+  const Stretch st = find_stretch<kTileT, kRowsT, 1>(a, blockIdx.x, gridDim.x);
+  if (blockIdx.x == 0)  // lengths that cannot be
+    for (int b = threadIdx.x; b < a.B; b += kThreadsT) {
+      const int ctx = a.context[b], cnt = a.count ? a.count[b] : a.T;
+      if (ctx < 0 || cnt < 0 || cnt > a.T ||
+          (long long)ctx + cnt > ((long long)a.c.table_pages << a.c.page_shift))
+        flag_bad(status, kWhereAttn);
+    }
+  if (st.s >= st.e) return;
   if (warp == kQkWarpT) tmem_alloc(&sm.tmem_base, kColsT);
   tc_fence_before();
   __syncthreads();
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), col_o = lanes + kColOT + sid * D;
     uint32_t swaps = 0;
     bool ok = true;
-    Place at = place_of<kTileT, kRowsT>(a, st.s);
+    Place at = place_of<kTileT, kRowsT>(a, st.own, st.s);
     for (unsigned seg = st.s; ok && seg < st.e;) {
       go_to<kTileT, kRowsT>(a, at, seg);
       const Unit u = unit_of(at, seg);
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 #pragma unroll
         for (int x = 0; x < DH / 8; ++x) {
           w[x] = make_uint4(0, 0, 0, 0);
-          if (row < rows) w[x] = __ldg(reinterpret_cast<const uint4*>(q + 8 * x));
+          if (row < rows) w[x] = *reinterpret_cast<const uint4*>(q + 8 * x);
           const uint32_t ww[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         top = max(top, sm.amax[sid ^ 1][row]);
         const int eq = q_exponent(top);
         const float down = __int_as_float((127 - eq) << 23);
-        f = q_factor(a.sl2, eq);
+        f = q_factor(eq);
 #pragma unroll
         for (int x0 = 0; x0 < DH / 8; x0 += 4) {
           uint32_t o[16];
@@ -430,22 +429,28 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           } else {
             const int64_t slot0 = (int64_t)(st.s + i - u.start) * kTileT;
             const int64_t d0 = slot0 - ctx;  // drafted token of the tile's first key (below 0: context)
+            const bool drafts = d0 < cnt && d0 > -kTileT;
+            const int lo = (int)max(d0, (int64_t)0), hi = drafts ? min((int)(d0 + kTileT), cnt) : lo;  // drafted tokens [lo, hi)
+            const int words = (a.T + 31) / 32, w0 = lo / 32, sh = lo % 32;
+            uint32_t m[4][3];  // the rows' mask words of lo and behind, all loads before the first use
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int rw = wrow + g + 8 * r, t = (row0 + rw) / a.G;
+#pragma unroll
+              for (int w = 0; w < 3; ++w)
+                m[r][w] = a.mask && drafts && rw < rows && w0 + w < words
+                              ? a.mask[((int64_t)b * a.T + t) * words + w0 + w] : 0u;
+            }
             uint32_t mine[2] = {0, 0};
             int E_new[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               uint64_t seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
-              if (wrow + g + 8 * r < rows && d0 < cnt && d0 > -64) {
-                const int lo = (int)max(d0, (int64_t)0), hi = min((int)(d0 + 64), cnt);  // drafted tokens [lo, hi)
+              if (wrow + g + 8 * r < rows && drafts) {
                 const int t = (row0 + wrow + g + 8 * r) / a.G;
                 uint64_t bits = 0;  // of tokens lo, lo + 1, ...
                 if (a.mask) {
-                  const int words = (a.T + 31) / 32;
-                  const uint32_t* m = a.mask + ((int64_t)b * a.T + t) * words;
-                  for (int w = lo / 32; w <= (hi - 1) / 32; ++w) {
-                    const uint64_t word = __ldg(m + w);
-                    bits |= 32 * w >= lo ? word << (32 * w - lo) : word >> (lo - 32 * w);
-                  }
+                  bits = (uint64_t)__funnelshift_r(m[r][1], m[r][2], sh) << 32 | __funnelshift_r(m[r][0], m[r][1], sh);
                 } else if (t >= lo) {
                   bits = t - lo >= 63 ? ~0ull : (2ull << (t - lo)) - 1;
                 }
@@ -563,7 +568,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         if (!wait(&sm.v_empty[i % kVStages], (i / kVStages) ^ 1, 8)) break;
         convert<D, VF>(smem_u32(sm.raw[r][1]), smem_u32(sm.v[i % kVStages]), w, lane, flags & kMasked);
       } else {
-        if (w == 0) {  // the softmax streams' V scales, seen behind k_full
+        if (w == 1) {  // the softmax streams' scales, seen behind k_full: K's with the softmax scale, and V's with 2^-E
+          sm.scale[slot][0][lane] *= a.sl2;
+          sm.scale[slot][0][lane + 32] *= a.sl2;
+        } else if (w == 0) {
           if (flags & kFirst) E = -126;
           if (!(flags & kMasked)) {
             const float v0 = sm.scale[slot][1][lane], v1 = sm.scale[slot][1][lane + 32];
@@ -590,7 +598,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     // of tile t of the next eight; the first group of a box stands for it.
     const int side = warp - kLoadK, box = min(1 << a.c.page_shift, kTileT), per = box / 16;
     const CUtensorMap* map = side ? &tm_v : &tm_k;
-    Place walk = place_of<kTileT, kRowsT>(a, st.s);
+    Place walk = place_of<kTileT, kRowsT>(a, st.own, st.s);
     int issued = 0, rows8 = -1;
     bool masked8 = false, first8 = false;
     for (int i = 0; i < n_tiles; ++i) {
@@ -634,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   } else {
     // -------------------------------------------------------------- issuers
     const uint32_t leader = lane == 0;
-    Place at = place_of<kTileT, kRowsT>(a, st.s);
+    Place at = place_of<kTileT, kRowsT>(a, st.own, st.s);
     unsigned seg_end = st.s;  // of the unit that tile i belongs to
     int units = 0, begin = 0;
     for (int i = 0; i < n_tiles; ++i) {
@@ -698,8 +706,7 @@ int launch_tc(const CacheAttnArgs& a, cudaStream_t s) {
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return SAGE_ERR_CUDA;
-  fn<<<kMaxCtas, kThreadsT, smem, s>>>(mk, mv, a);
-  if (cudaGetLastError() != cudaSuccess) return SAGE_ERR_CUDA;
+  if (const int rc = launch_dependent(fn, dim3(kMaxCtas), kThreadsT, smem, s, mk, mv, a)) return rc;
   return launch_join<kTileT, kRowsT, D, 1>(a, s);
 }
 

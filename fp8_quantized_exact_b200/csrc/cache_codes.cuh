@@ -86,10 +86,10 @@ __device__ __forceinline__ uint32_t swizzled(int key, int chunk) {
 __device__ __forceinline__ int q_exponent(uint32_t top) {
   return (top == 0 || top >= 0x7F80u) ? 0 : max((int)(top >> 7) - 127 - 13, -110);
 }
-// The factor of the row's raw scores (base 2).
-__device__ __forceinline__ float q_factor(float sl2, int eq) {
-  return fmaxf(sl2 * __int_as_float((127 + eq) << 23), 1.17549435e-38f);
-}
+// The factor of the row's scores, which hold sm_scale log2 e already (it goes to the key's scale): a power of two, so that
+// x f - c is the difference of two scores without a rounding of either product.  With sm_scale in f the fused x f - c
+// kept what rounding had taken from c, which passes 2^16 from scores of 2^40 on.
+__device__ __forceinline__ float q_factor(int eq) { return __int_as_float((127 + eq) << 23); }
 
 constexpr float kRaise = 8.0f;  // a row's offset is raised for scores that pass it by more (log2)
 

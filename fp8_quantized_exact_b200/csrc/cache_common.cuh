@@ -5,6 +5,30 @@
 
 namespace sage {
 
+// The serving kernels are short and follow one another, so each is launched as a programmatic dependent of what is before
+// it on its stream: its blocks become resident while that drains, prepare what needs no input, and wait in
+// `begin_dependent` until it has completed and its writes are visible.  What follows is let on only behind that wait,
+// so at most two of these kernels overlap, and no block of a later one is resident before the one two
+// back has ended.  Inputs are read by plain loads: the read-only path is for what nobody writes during a kernel's life.
+__device__ __forceinline__ void begin_dependent() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+}
+
 // One tensor of a rotary call: input and output with element strides.
 struct RopeSide {
   const uint16_t* x;
@@ -50,7 +74,7 @@ __device__ __forceinline__ void flag_bad(DeviceStatus* st, int where) {
 // head h, or -1 where the slot is behind the table or its entry names no page.
 __device__ __forceinline__ int64_t cache_row(const CacheArgs& c, int b, int h, int64_t slot) {
   if (slot < 0 || (slot >> c.page_shift) >= c.table_pages) return -1;
-  const int page = __ldg(c.table + (int64_t)b * c.table_pages + (int)(slot >> c.page_shift));
+  const int page = c.table[(int64_t)b * c.table_pages + (int)(slot >> c.page_shift)];
   if (page < 0 || page >= c.pages) return -1;
   return (((int64_t)page * c.H + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
 }

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
   const int half_rot = a.rot / 2, pitch = (half_rot + 1) & ~1;  // 16-byte reads of two
   const unsigned tok0 = blockIdx.x * (unsigned)toks;
   const int nt = (int)min((unsigned)toks, (unsigned)(a.B * a.N) - tok0);
+  begin_dependent();
   for (int i = threadIdx.x; i < nt * half_rot; i += kRopeThreads) {
     const int t = i / half_rot, j = i - t * half_rot;
     const unsigned b = (tok0 + t) / (unsigned)a.N, n = (tok0 + t) - b * a.N;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
 }
 
 template <bool HALF>
-void run(const RopeArgs& a, cudaStream_t s) {
+int run(const RopeArgs& a, cudaStream_t s) {
   const int64_t tokens = (int64_t)a.B * a.N;
   const int H = a.Hq + a.Hk;
   const bool vec = a.rot % (HALF ? 16 : 8) == 0;
@@ -188,16 +189,14 @@ void run(const RopeArgs& a, cudaStream_t s) {
   while (heads > 4 && groups * ((H + heads - 1) / heads) < 2 * 148) heads = (heads + 1) / 2;
   const dim3 grid((unsigned)groups, (H + heads - 1) / heads);
   const size_t smem = (size_t)toks * (sizeof(TokenRows) + ((a.rot / 2 + 1) & ~1) * sizeof(float2));
-  if (vec) rope_kernel<HALF, true><<<grid, kRopeThreads, smem, s>>>(a, toks, heads, items, rot_items, shift);
-  else rope_kernel<HALF, false><<<grid, kRopeThreads, smem, s>>>(a, toks, heads, items, rot_items, shift);
+  return launch_dependent(vec ? rope_kernel<HALF, true> : rope_kernel<HALF, false>, grid, kRopeThreads, smem, s, a, toks, heads,
+                          items, rot_items, shift);
 }
 
 }  // namespace
 
 int launch_rope(const RopeArgs& a, cudaStream_t s) {
-  if (a.half) run<true>(a, s);
-  else run<false>(a, s);
-  return cudaGetLastError() == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+  return a.half ? run<true>(a, s) : run<false>(a, s);
 }
 
 }  // namespace sage

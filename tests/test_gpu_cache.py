@@ -641,3 +641,41 @@ def test_binding_refusals(sage, ws):
             call()
     with pytest.raises(sage.SageError):
         sage.sage_cache_attn(q, cache, table, c, None, None, out, lse, 0.0, ws[:512])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(1, 4), (2, 8), (24, 8)])
+@pytest.mark.parametrize("power", [4, 20, 28, 32, 36, 44, 60, 100])
+def test_attn_scores_of_any_size(sage, ws, power, T, G, D):
+    """Scores of +-D^0.5 2^power: two equal keys of the largest score share the row, however large it is.  The others are
+    at most half of it, below by 2^power D^0.5 / 2 >= 64, and leave nothing (e^-64).  w has 2^-11, exp2 and the sums 2^-19,
+    the result 2^-8; lse the score's (D + 4) 2^-24, relative here since every product has the sign of the sum."""
+    B, H, page, ctx = 2, 2, 32, 1500
+    n = ctx + T
+    per = -(-n // page)
+    cache = empty_cache(sage, B * per, H, page, D, INT8, E4M3)
+    table = make_table(B, per, B * per, [n] * B, page, seed=power)
+    rng = gen(power + T)
+    u = torch.where(torch.rand(D, generator=rng) < 0.5, -1.0, 1.0).to(DEV)
+    r = (torch.rand(B, n, H, generator=rng) * 1.5 - 1.0).to(DEV)  # below 0.5
+    top = [[5, ctx - 3], [40, 777]]
+    for b in range(B):
+        r[b, top[b]] = 1.0
+    a = power // 2
+    k = (r[..., None] * u * 2.0 ** (power - a)).bfloat16()
+    v = rand(B, n, H, D, seed=power)
+    q = (u * 2.0 ** a).bfloat16().expand(B, T, H * G, D).contiguous()
+    sage.sage_cache_append(cache, k, v, table, None, None, ws)
+    out = torch.empty_like(q)
+    lse = torch.empty(B, T, H * G, device=DEV)
+    sage.sage_cache_attn(q, cache, table, i32(*[ctx] * B), None, None, out, lse, 0.0, ws)
+    assert status(sage, ws) == sage.SAGE_OK
+    for b in range(B):
+        kk, vv = cu.rows(cache, table, b, torch.tensor(top[b], device=DEV))
+        want = vv.mean(0).repeat_interleave(G, 0).expand(T, H * G, D)
+        spread = vv.abs().mean(0).repeat_interleave(G, 0).expand(T, H * G, D)
+        err = (out[b].double() - want).abs()
+        assert (err <= spread * (2.0 ** -11 + 2.0 ** -18) + 2.0 ** -8 * want.abs()).all(), float(err.max())
+        s = (q[b, 0, ::G].double() * kk[0]).sum(-1) * D ** -0.5 + math.log(2.0)
+        got = lse[b].double().view(T, H, G)
+        assert ((got - s[None, :, None]).abs() <= s.abs()[None, :, None] * (D + 8) * 2.0 ** -24).all()
