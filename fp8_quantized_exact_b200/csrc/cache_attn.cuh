@@ -63,6 +63,8 @@ __device__ __forceinline__ Unit unit_of(const Place& p, unsigned idx) {
   return r;
 }
 
+constexpr unsigned kMaxParts = 32;  // of a unit of many rows
+
 // The stretch [s, e) of CTA `cta` of `ctas`, and the place of a tile in it.
 // Every warp finds it for itself, 32 sequences at a time, which needs no
 // barrier.  STEP: stretches are multiples of it.
@@ -78,10 +80,18 @@ __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta,
   t.own.n = t.own.rt = 1;
   t.own.per = 0;
   if (lane < a.B) t.own = seq_of<TILE, R>(a, lane);
-  unsigned sum = t.own.per;
-  for (int b = lane + 32; b < a.B; b += 32) sum += seq_of<TILE, R>(a, b).per;
+  unsigned sum = t.own.per, longest = t.own.n;
+  for (int b = lane + 32; b < a.B; b += 32) {
+    const Seq s = seq_of<TILE, R>(a, b);
+    sum += s.per;
+    longest = max(longest, s.n);
+  }
   t.total = __reduce_add_sync(0xffffffffu, sum);
   t.share = max((t.total + ctas * STEP - 1) / (ctas * STEP), 1u) * STEP;
+  // Many rows: a part of a unit is up to 64 KB, and the join reads all parts of a unit in one block per 8 rows, so a
+  // short list is cut into fewer.  Measured on B200 (us, one unit of 128 rows over 128 tiles of 64 keys): 128 parts
+  // 56, 43 33.5, 32 28.9, 22 30.4; units of 2 tiles are cut in two as before.
+  if (R >= 64) t.share = max(t.share, (__reduce_max_sync(0xffffffffu, longest) + kMaxParts - 1) / kMaxParts);
   t.s = min((unsigned)cta * t.share, t.total);
   t.e = min(t.s + t.share, t.total);
   return t;
@@ -121,12 +131,14 @@ __device__ __forceinline__ Place place_of(const CacheAttnArgs& a, const Seq& own
   return p;  // not reached for idx below the list's end
 }
 
-// The longest list that the arguments allow has to stay below 2^31 tiles.
+// The longest list that the arguments allow, in tiles; it has to stay below 2^31.
 template <int TILE, int R>
-inline bool list_fits(const CacheAttnArgs& a) {
+inline double longest_list(const CacheAttnArgs& a) {
   const double n = (((double)a.c.table_pages * (1 << a.c.page_shift)) + TILE - 1) / TILE;
-  return n * a.B * a.c.H * ((a.T * a.G + R - 1) / R) < 2147483648.0;
+  return n * a.B * a.c.H * ((a.T * a.G + R - 1) / R);
 }
+template <int TILE, int R>
+inline bool list_fits(const CacheAttnArgs& a) { return longest_list<TILE, R>(a) < 2147483648.0; }
 
 // begin_dependent, also for codes that a kernel before wrote by ordinary stores and TMA reads.
 __device__ __forceinline__ void begin_dependent_tma() {
@@ -175,14 +187,23 @@ __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, int b, int h, 
 }
 
 // Joins the parts of the unit that begins in CTA blockIdx.x's stretch and is
-// cut by its end; blockIdx.y of gridDim.y takes a share of the rows.  The
+// cut by its end; blockIdx.y takes kRows of its rows.  Threads beyond a float4 of each share the
+// parts, group by group in list order, so the sums have one order.  The
 // blocks find their unit while the CTAs of the main kernel end, and wait for them.
-constexpr int kJoinThreads = 128;
+template <int R, int D>
+struct Join {
+  // few rows: more threads for each, since one unit may have a part in every CTA; many: a grid that stays within a
+  // resident wave
+  static constexpr int kRows = R >= 64 ? 8 : 4, kThreads = 256, kItems = kRows * D / 4, kGroups = kThreads / kItems;
+  static_assert(kThreads % kItems == 0 && R % kRows == 0, "whole groups and blocks");
+};
 template <int TILE, int R, int D, int STEP>
-__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const CacheAttnArgs a, int ctas) {
-  constexpr int RB = 8;  // rows at a time
+__global__ void __launch_bounds__(256) cache_attn_join_kernel(const CacheAttnArgs a, int ctas) {
+  using J = Join<R, D>;
+  constexpr int RB = J::kRows, V4 = D / 4;
   __shared__ float c_s[RB][kMaxCtas], l_s[RB][kMaxCtas];  // offsets, then weights; denominators
   __shared__ float c_row[RB], l_row[RB];
+  __shared__ float4 o_s[J::kGroups > 1 ? J::kThreads : 1];
   // the lengths are older than the kernel in front, which waited for them
   const Stretch st = find_stretch<TILE, R, STEP>(a, blockIdx.x, ctas);
   Place p;
@@ -196,58 +217,69 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const Cac
   begin_dependent();
   if (st.s >= st.e || u.start < st.s || end <= st.e) return;
   const int first = blockIdx.x, np = (int)((end - 1) / st.share) - first + 1;
-  const int rows = min(R, p.s.cnt * a.G - u.rt * R);
+  const int r0 = blockIdx.y * RB, nr = min(RB, min(R, p.s.cnt * a.G - u.rt * R) - r0);
+  if (nr <= 0) return;
   auto part = [&](int i) { return part_of<R, D>(a, first + i, i == 0 ? 1 : 0); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r0 = blockIdx.y * RB; r0 < rows; r0 += gridDim.y * RB) {
-    const int nr = min(RB, rows - r0);
-    for (int i = threadIdx.x; i < np * RB; i += kJoinThreads) {
-      const int k = i / RB, r = i % RB;
-      if (r < nr) {
-        c_s[r][k] = part(k)[R * D + r0 + r];
-        l_s[r][k] = part(k)[R * D + R + r0 + r];
-      }
+  for (int i = threadIdx.x; i < np * RB; i += J::kThreads) {
+    const int k = i / RB, r = i % RB;
+    if (r < nr) {
+      c_s[r][k] = part(k)[R * D + r0 + r];
+      l_s[r][k] = part(k)[R * D + R + r0 + r];
     }
-    __syncthreads();
-    for (int r = warp; r < nr; r += kJoinThreads / 32) {
-      float c = -INFINITY, l = 0.0f;
-      for (int k = lane; k < np; k += 32) c = fmaxf(c, c_s[r][k]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
-      for (int k = lane; k < np; k += 32) {
-        const float f = c_s[r][k] == -INFINITY ? 0.0f : ex2f(c_s[r][k] - c);
-        l += l_s[r][k] * f;
-        c_s[r][k] = f;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == 0) {
-        c_row[r] = c;
-        l_row[r] = l;
-      }
-    }
-    __syncthreads();
-    constexpr int V4 = D / 4;
-    for (int i4 = threadIdx.x; i4 < nr * V4; i4 += kJoinThreads) {
-      const int r = i4 / V4, col = 4 * (i4 % V4);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int k = 0; k < np; ++k) {
-        const float f = c_s[r][k];
-        const float4 x = *reinterpret_cast<const float4*>(part(k) + (r0 + r) * D + col);
-        o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
-      }
-      store_out(a, p.b, u.h, u.rt * R + r0 + r, col, o, row_inverse(l_row[r]));
-      if (col == 0) store_lse(a, p.b, u.h, u.rt * R + r0 + r, c_row[r], l_row[r]);
-    }
-    __syncthreads();
   }
+  __syncthreads();
+  if (warp < nr) {
+    const int r = warp;
+    float c = -INFINITY, l = 0.0f;
+    for (int k = lane; k < np; k += 32) c = fmaxf(c, c_s[r][k]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, o));
+    for (int k = lane; k < np; k += 32) {
+      const float f = c_s[r][k] == -INFINITY ? 0.0f : ex2f(c_s[r][k] - c);
+      l += l_s[r][k] * f;
+      c_s[r][k] = f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      c_row[r] = c;
+      l_row[r] = l;
+    }
+  }
+  __syncthreads();
+  const int i4 = threadIdx.x % J::kItems, group = threadIdx.x / J::kItems, r = i4 / V4, col = 4 * (i4 % V4);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (r < nr) {
+#pragma unroll 8
+    for (int k = group; k < np; k += J::kGroups) {
+      const float f = c_s[r][k];
+      const float4 x = *reinterpret_cast<const float4*>(part(k) + (r0 + r) * D + col);
+      o.x += x.x * f; o.y += x.y * f; o.z += x.z * f; o.w += x.w * f;
+    }
+  }
+  if (J::kGroups > 1) {
+    o_s[threadIdx.x] = o;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int k = 1; k < J::kGroups; ++k) {
+      const float4 x = o_s[k * J::kItems + i4];
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    }
+  }
+  if (r >= nr) return;
+  store_out(a, p.b, u.h, u.rt * R + r0 + r, col, o, row_inverse(l_row[r]));
+  if (col == 0) store_lse(a, p.b, u.h, u.rt * R + r0 + r, c_row[r], l_row[r]);
 }
 
 template <int TILE, int R, int D, int STEP>
 int launch_join(const CacheAttnArgs& a, cudaStream_t s) {
-  return launch_dependent(cache_attn_join_kernel<TILE, R, D, STEP>, dim3(kMaxCtas, R >= 64 ? 4 : 1), kJoinThreads, 0, s, a,
-                          kMaxCtas);
+  using J = Join<R, D>;
+  const int rows = min(R, a.T * a.G);                                                // of the fullest unit
+  const int ctas = (int)fmin(kMaxCtas, ceil(longest_list<TILE, R>(a) / STEP));  // that can have a stretch
+  return launch_dependent(cache_attn_join_kernel<TILE, R, D, STEP>, dim3(ctas, (rows + J::kRows - 1) / J::kRows),
+                          J::kThreads, 0, s, a, kMaxCtas);
 }
 
 }  // namespace cattn

@@ -401,7 +401,9 @@ SAGE_API int sage_debug_qk_s32(const int8_t* q_i8, const float* q_scale, const i
  * new or drafted tokens over it (no counterpart in the pages: the quantised
  * tensors above are made anew by every call; these keep them between calls,
  * one token at a time).  A step of a serving loop is sage_rope on the new Q
- * and K, sage_cache_append, sage_cache_attn.
+ * and K, sage_cache_append, sage_cache_attn.  Each call's kernels may become
+ * resident before what is in front of them on the stream has ended, and wait
+ * for it on the device: stream order holds as for any other kernel.
  *
  * The cache.  Every token has, per head, D codes of K and of V and one FP32
  * scale for each; nothing is shared between tokens, so a token is appended
@@ -523,8 +525,8 @@ SAGE_API int sage_cache_read(const sage_cache* cache, const int32_t* page_table,
  *     rounded to FP16.
  *   - lse (NULL or [B][T][Hq]): ln sum_j exp(s_j).
  *   - A row that sees nothing: out 0, lse -inf.
- * Masked and unused slots may hold any bytes.  Workspace:
- * sage_workspace_bytes(SAGE_OP_CACHE_ATTN, ...). */
+ * Masked and unused slots may hold any bytes.  out and lse must not overlap the
+ * inputs.  Workspace: sage_workspace_bytes(SAGE_OP_CACHE_ATTN, ...). */
 SAGE_API int sage_cache_attn(sage_view_bf16 q, const sage_cache* cache, const int32_t* page_table, int table_pages,
                              const int32_t* context, const int32_t* count, const uint32_t* mask, void* out,
                              int64_t out_stride_b, int64_t out_stride_n, int64_t out_stride_h, float* lse, int B,
