@@ -24,7 +24,7 @@
 // keys takes about 1,900 cycles on an SM at 128 rows (tensor pipe 26% busy, issue
 // slots 46%) and little less at 16 rows; an M = 128 MMA costs its issuer about 65
 // cycles for any N up to 128.  Tried and not kept, as factors of the time of 64 drafted
-// tokens over 4 contexts of 20000..37810 (424 us): pairs of tiles per QK MMA 1.27, P in
+// tokens over 4 contexts of 20000..37810 (424 us then, 409 now): pairs of tiles per QK MMA 1.27, P in
 // columns of its own with Q in shared memory 1.05, one QK issuer per stream 1.25,
 // both score loads of a half before one wait 1.12, two converter warps per side
 // instead of four 1.22, 32x32b loads with every scale read by every thread 1.15.
