@@ -143,3 +143,57 @@ def test_first_call_of_a_process_may_be_captured(sage, tmp_path):
         "torch.cuda.synchronize()\n"
         "assert (out == 1).all() and s.sage_read_device_status(ws) == 0\n")
     subprocess.run([sys.executable, str(src)], check=True, timeout=300)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("N,H,D", [(150, 2, 128), (700, 4, 64), (2000, 3, 128)])
+def test_chain_with_the_full_attention(sage, N, H, D, captured):
+    """Cache and rotary calls between full attentions, whose own kernels start early too: each reads what the one in
+    front wrote, and the rotary call and the read write what it has just read."""
+    g = torch.Generator("cuda").manual_seed(N)
+    first = torch.randn(3, 1, N, H, D, device="cuda", generator=g).bfloat16()
+    pages = -(-N // 32)
+    table = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)[None].contiguous()
+    freq, mscale = sage.sage_rope_freqs(D)
+    ws = sage.workspace(sage.SAGE_OP_CACHE, 1, 1, 1, D)
+    full_ws = sage.workspace(sage.SAGE_OP_ATTN_FWD, 1, N, H, D)
+
+    def chain(between, x, cache, out):
+        q, k, v = x
+        sage.sage_rope(q, k, q, k, None, freq, mscale)
+        between()
+        sage.sage_cache_append(cache, k, v, table, None, None, ws)
+        between()
+        sage.sage_cache_read(cache, table, None, None, k, v, ws)
+        between()
+        sage.sage_attn_fwd(q, k, v, out, 0.0, full_ws)
+        between()
+        sage.sage_rope(out, k, q, k, None, freq, mscale, inverse=True)
+        between()
+        sage.sage_attn_fwd(q, k, v, out, 0.0, full_ws)
+        between()
+        sage.sage_cache_append(cache, out, k, table, None, None, ws)
+        between()
+        sage.sage_cache_read(cache, table, None, None, v, q, ws)
+        between()
+
+    results = []
+    for sync in (True, False):
+        x, out = [t.clone() for t in first], torch.empty_like(first[0])
+        cache = sage.cache_buffers(pages, H, 32, D)
+        between = torch.cuda.synchronize if sync else lambda: None
+        torch.cuda.synchronize()
+        if captured and not sync:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                chain(between, x, cache, out)
+            for _ in range(8):
+                graph.replay()
+        else:
+            for _ in range(8):
+                chain(between, x, cache, out)
+        torch.cuda.synchronize()
+        assert sage.sage_read_device_status(ws) == sage.SAGE_OK
+        results.append([t.clone() for t in (*x, out)])
+    assert all(torch.isfinite(t).all() for t in results[0])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
