@@ -679,3 +679,14 @@ def test_attn_scores_of_any_size(sage, ws, power, T, G, D):
         s = (q[b, 0, ::G].double() * kk[0]).sum(-1) * D ** -0.5 + math.log(2.0)
         got = lse[b].double().view(T, H, G)
         assert ((got - s[None, :, None]).abs() <= s.abs()[None, :, None] * (D + 8) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("T,G,D", [(1, 4, 128), (1, 8, 64), (2, 8, 64), (4, 4, 128), (40, 4, 128), (33, 2, 64)])
+@pytest.mark.parametrize("n", [300, 2100, 20011])
+def test_attn_one_head_cut_into_many_parts(sage, ws, T, G, D, n):
+    """One sequence and one head: every CTA has a part of the same unit, or of the same few."""
+    cache, table = filled(sage, [n + T], 1, 16, D, INT8, E4M3, seed=n + T)
+    q = rand(1, T, G, D, seed=n)
+    out, lse = run_attn(sage, ws, q, cache, table, i32(n), None, None)
+    assert status(sage, ws) == sage.SAGE_OK
+    check_attn(q, cache, table, i32(n), None, None, out, lse)
