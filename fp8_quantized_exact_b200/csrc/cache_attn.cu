@@ -14,12 +14,13 @@
 // down to 2^-27 of the largest.
 //
 // Online softmax per row in base 2: FP32 sums l += p_j and O += w_j code_j,
-// p_j = 2^(s_j - c) and w_j = p_j vscale_j 2^-E rounded to FP16 (2^-11).  The
-// offset c is the largest score at the row's last update and is raised only when
-// a score passes it by more than 8 (so p_j <= 2^8), which one vote per tile finds
-// out: later tiles need no reduction across lanes.  E is an integer per row with
-// 2^E at or above the largest V scale that the row has seen; it is per row
-// because a token that only other rows see may have any scale.
+// p_j = 2^(s_j - c) and w_j = p_j vscale_j 2^-E rounded to FP16 (2^-11), for which
+// c keeps the row's largest weight near 2^10 (cache_codes.cuh says why).  c is set
+// again only when a score passes it by more than 15 or a V scale passes 2^E, which
+// one vote per tile finds out: later tiles need no reduction across lanes.  E is an
+// integer per row with 2^E at or above the largest V scale that the row has seen; it
+// is per row because a token that only other rows see may have any scale.  When E
+// grows, c falls by as much, which leaves the unit of O.
 //
 // One CTA per SM.  A CTA's stretch of the work list is cut once more, into one
 // stretch per warp, and the warps run alone: lane 0 keeps its ring of K and V
@@ -287,7 +288,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
           const int key = 16 * hf + 8 * j + key_of(g);
           const float kk = __shfl_sync(0xffffffffu, ks, key);
           vsc[hf][j] = __shfl_sync(0xffffffffu, vs, key);
-          vtop = fmaxf(vtop, vsc[hf][j]);
+          if (!MASKED) vtop = fmaxf(vtop, vsc[hf][j]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 x = unpair(mul2(pair(s[hf][nt][2 * j], s[hf][nt][2 * j + 1]), pair(kk, kk)));
@@ -336,8 +337,13 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
                 else s[hf][nt][2 * j + e] = -INFINITY;
               }
           }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)  // a key that one of the thread's rows sees
+            if (seen & (0x03030303u << (hf * 4 + j * 2))) vtop = fmaxf(vtop, vsc[hf][j]);
       }
-      bool up = MASKED || vtop > vlim;
+      bool up = vtop > vlim;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -345,37 +351,64 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
           up |= fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e])) > rs[nt].thr[e];
       if (__any_sync(0xffffffffu, up)) {
         vlim = INFINITY;
+        if (!MASKED) {
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, k));
+        }
+        float lv[2][2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) lv[hf][j] = lg2f(vsc[hf][j]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float al_o[2], al_l[2], nc[2], dn[2];
           const float2 f = unpair(rs[nt].f), nc_old = unpair(rs[nt].nc), dn_old = unpair(rs[nt].down);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = -INFINITY, vm = 0.0f;
+            float top = -INFINITY, weight = -INFINITY, vm = vtop;  // vm: the largest V scale that the row sees
+            if (MASKED) {
+              vm = 0.0f;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if ((seen >> (nt * 8 + hf * 4 + j * 2 + e)) & 1u) vm = fmaxf(vm, vsc[hf][j]);
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
+            }
+            const float fe = e ? f.y : f.x, c_old = -(e ? nc_old.y : nc_old.x), d_old = e ? dn_old.y : dn_old.x;
+            const int E_old = 127 - (__float_as_int(d_old) >> 23);
+            const int E = min(max(E_old, (__float_as_int(vm) >> 23) - 126), 126);
+            dn[e] = __int_as_float((127 - E) << 23);
+            vlim = fminf(vlim, __int_as_float((127 + E) << 23));
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int j = 0; j < 2; ++j) {  // a score that the row does not see is -infinity
                 top = fmaxf(top, s[hf][nt][2 * j + e]);
-                if ((seen >> (nt * 8 + hf * 4 + j * 2 + e)) & 1u) vm = fmaxf(vm, vsc[hf][j]);
+                weight = fmaxf(weight, __fmaf_ru(s[hf][nt][2 * j + e], fe, lv[hf][j]));
               }
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) {
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
+              weight = fmaxf(weight, __shfl_xor_sync(0xffffffffu, weight, k));
             }
-            const float fe = e ? f.y : f.x, c_old = -(e ? nc_old.y : nc_old.x);
             const bool none = rs[nt].thr[e] == -INFINITY;
-            const float c = none ? (top == -INFINITY ? 0.0f : top * fe) : fmaxf(c_old, top * fe);
+            float c = top == -INFINITY ? (none ? 0.0f : -INFINITY) : tile_offset(top * fe, weight, E);
+            if (__any_sync(0xffffffffu, !none && E != E_old)) {
+              const float2 l2 = unpair(rs[nt].l);
+              float mass = e ? l2.y : l2.x;
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) mass += __shfl_xor_sync(0xffffffffu, mass, k);
+              if (!none) c = fmaxf(c, kept_offset(c_old, E - E_old, mass));
+            } else if (!none) {
+              c = fmaxf(c, c_old);
+            }
             al_l[e] = none ? 0.0f : ex2f(c_old - c);
-            if (top != -INFINITY && (none || c > c_old)) rs[nt].thr[e] = __fadd_rd(top, kRaise / fe);
-            const float d_old = e ? dn_old.y : dn_old.x;
-            const int E_old = 127 - (__float_as_int(d_old) >> 23);
-            const int E = min(max(E_old, (__float_as_int(vm) >> 23) - 126), 126);
-            dn[e] = __int_as_float((127 - E) << 23);
-            al_o[e] = E == E_old ? al_l[e] : al_l[e] * ex2f((float)(E_old - E));
+            al_o[e] = none ? 0.0f : ex2f((c_old - c) + (float)(E_old - E));
+            if (!none || top != -INFINITY) rs[nt].thr[e] = __fadd_rd(c, kLimit) / fe;
             nc[e] = -c;
-            vlim = fminf(vlim, __int_as_float((127 + E) << 23));
           }
           rs[nt].nc = pair(nc[0], nc[1]);
           rs[nt].down = pair(dn[0], dn[1]);
@@ -467,25 +500,25 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int lr = 8 * nt + 2 * c4 + e;
-        const float l = e ? l2.y : l2.x, up = __int_as_float((254 << 23) - __float_as_int(e ? dn.y : dn.x));  // 2^E
-        const float c = rs[nt].thr[e] == -INFINITY ? -INFINITY : -(e ? nc.y : nc.x);
+        const float up = __int_as_float((254 << 23) - __float_as_int(e ? dn.y : dn.x));  // 2^E
+        const Mass m = normalised(rs[nt].thr[e] == -INFINITY ? -INFINITY : -(e ? nc.y : nc.x), e ? l2.y : l2.x);
         if (lr >= rows) continue;
         if (whole) {
           const OutRow to(a, b, h, row0 + lr);
-          const float f = row_inverse(l);
+          const float f = m.g * row_inverse(m.l);
 #pragma unroll
           for (int x = 0; x < XV; ++x)
             *reinterpret_cast<uint32_t*>(to.p + 16 * x + 2 * g) =
-                pack_bf16x2(o[nt][x][e] * up * f, o[nt][x][2 + e] * up * f);
-          if (g == 0) store_lse(a, b, h, row0 + lr, c, l);
+                pack_bf16x2(o[nt][x][e] * f * up, o[nt][x][2 + e] * f * up);
+          if (g == 0) store_lse(a, b, h, row0 + lr, m.c, m.l);
         } else {
 #pragma unroll
           for (int x = 0; x < XV; ++x)
             *reinterpret_cast<float2*>(part + lr * D + 16 * x + 2 * g) =
-                make_float2(o[nt][x][e] * up, o[nt][x][2 + e] * up);
+                make_float2(o[nt][x][e] * m.g * up, o[nt][x][2 + e] * m.g * up);
           if (g == 0) {
-            sm.c[warp][slot][lr] = c;
-            sm.l[warp][slot][lr] = l;
+            sm.c[warp][slot][lr] = m.c;
+            sm.l[warp][slot][lr] = m.l;
           }
         }
       }

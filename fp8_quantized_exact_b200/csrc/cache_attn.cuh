@@ -11,6 +11,7 @@
 // its stretch, slot 1 for one that begins in it and goes on behind it.  The
 // lengths are read on the device, so a captured launch follows them.
 #pragma once
+#include "cache_codes.cuh"
 #include "cache_common.cuh"
 
 namespace sage {
@@ -161,6 +162,11 @@ __device__ __forceinline__ float ex2f(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float lg2f(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -183,7 +189,8 @@ __device__ __forceinline__ float row_inverse(float l) { return l == 0.0f ? 0.0f 
 __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, int b, int h, int row, float c, float l) {
   if (!a.lse) return;
   const int t = row / a.G, hq = h * a.G + row % a.G;
-  a.lse[((int64_t)b * a.T + t) * a.Hq + hq] = l == 0.0f ? -INFINITY : (c + log2f(l)) * 0.693147180559945f;
+  const Mass m = normalised(c, l);
+  a.lse[((int64_t)b * a.T + t) * a.Hq + hq] = l == 0.0f ? -INFINITY : (m.c + log2f(m.l)) * 0.693147180559945f;
 }
 
 // Joins the parts of the unit that begins in CTA blockIdx.x's stretch and is

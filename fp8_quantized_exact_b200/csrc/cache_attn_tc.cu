@@ -3,7 +3,7 @@
 //
 // The mathematics is that of cache_attn.cu: S = Q K^T and O = P V with the codes
 // exact in FP16, Q rows scaled by a power of two, FP32 statistics, a lazily
-// raised offset c, probabilities times V scales 2^-E rounded to FP16.  Here a
+// set offset c, probabilities times V scales 2^-E rounded to FP16.  Here a
 // unit is up to 128 rows, the M of the MMAs, and a tile is 64 keys.
 //
 // One CTA per SM, with fixed roles:
@@ -62,9 +62,10 @@ struct SmemT {
   alignas(1024) uint8_t raw[kRaw][2][kTileT * D];
   alignas(128) float scale[kScales][2][kTileT];
   alignas(16) float vd[kScales][kTileT];  // V scales times 2^-E of the tile (tiles that every row sees whole)
+  alignas(16) float lv[kScales][kTileT];  // log2 of the V scales
   int e[kScales];                       // that E
   uint32_t amax[2][kRowsT];             // of the halves of Q's rows
-  float c[2][kRowsT], l[2][kRowsT], up[2][kRowsT];  // what the streams exchange at a unit's end
+  float c[2][kRowsT], l[2][kRowsT], g[2][kRowsT], up[2][kRowsT];  // what the streams exchange at a unit's end
   int flags[kScales];                   // bits 0-3: the 16-key groups that hold keys; bit 4: not every row sees every key; bit 5: a unit's first tile
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
@@ -116,6 +117,16 @@ __device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16])
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+// Two blocks, waited for.
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -182,10 +193,241 @@ __device__ __forceinline__ void convert(uint32_t raw, uint32_t to, int w, int la
   }
 }
 
+// The offsets c of a thread's two rows (of 16, at TMEM columns `cols`) for a tile, the sums l in their unit, and the factors
+// al of the accumulator's rows; `ks`, `lv`: the keys' score scales and log2 of their V scales; bit 16 q + 2 n + e of `seen`:
+// row q sees key 8 n + 2 c4 + e; bit q of `none`: row q has seen nothing yet, of `found`: it has now.  Rare (a unit's first
+// tile in each stream, a larger V scale), and it pays by its size: unrolled, or 32 keys at a time, its four
+// copies cost the common path more (us, 21 drafted tokens over 16 contexts of 500..16384: 16 keys at a time 184, 8
+// keys 190, 32 keys 193, unrolled 252).
+struct Offsets {
+  float c[2], l[2], al[2];
+  uint32_t found;
+};
+__device__ __forceinline__ Offsets set_offsets(uint32_t cols, const float* ks, const float* lv, uint32_t seen, uint32_t none,
+                                               float fr0, float fr1, const Offsets& was, int E0, int E1, int Ea, int Eb) {
+  const float fr[2] = {fr0, fr1};
+  const int E[2] = {E0, E1}, E_new[2] = {Ea, Eb};
+  float top[2] = {-INFINITY, -INFINITY}, weight[2] = {-INFINITY, -INFINITY};
+  uint32_t s[8];
+#pragma unroll 1
+  for (int cb = 0; cb < 4; ++cb) {
+    tmem_ld_frag2(cols + 16 * cb, s);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int n = 2 * cb + m;
+      const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n), v2 = *reinterpret_cast<const float2*>(lv + 8 * n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((seen >> (16 * (e >> 1) + 2 * n + (e & 1))) & 1u) {
+          const float x = __uint_as_float(s[4 * m + e]) * ((e & 1) ? k2.y : k2.x);
+          top[e >> 1] = fmaxf(top[e >> 1], x);
+          weight[e >> 1] = fmaxf(weight[e >> 1], __fmaf_ru(x, fr[e >> 1], (e & 1) ? v2.y : v2.x));
+        }
+    }
+  }
+  Offsets to;
+  to.found = 0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    float mass = was.l[q];
+#pragma unroll
+    for (int k = 1; k < 4; k <<= 1) {  // the four threads that share a row
+      mass += __shfl_xor_sync(0xffffffffu, mass, k);
+      top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], k));
+      weight[q] = fmaxf(weight[q], __shfl_xor_sync(0xffffffffu, weight[q], k));
+    }
+    const bool nothing = (none >> q) & 1u, some = top[q] != -INFINITY;
+    const float kept = kept_offset(was.c[q], E_new[q] - E[q], mass);
+    const float set = some ? tile_offset(top[q] * fr[q], weight[q], E_new[q]) : nothing ? 0.0f : kept;
+    to.c[q] = nothing ? set : fmaxf(set, kept);
+    to.l[q] = nothing ? 0.0f : was.l[q] * ex2(was.c[q] - to.c[q]);
+    to.al[q] = nothing ? 0.0f : ex2((was.c[q] - to.c[q]) + (float)(E[q] - E_new[q]));
+    if (some) to.found |= 1u << q;
+  }
+  return to;
+}
+// Multiplies a thread's two rows of an accumulator at TMEM columns `col` on.
+template <int D>
+__device__ __forceinline__ void multiply_rows(uint32_t col, float al0, float al1) {
+  uint32_t s[16];
+#pragma unroll 1
+  for (int x = 0; x < D; x += 32) {
+    tmem_ld_frag4(col + x, s);
+    tmem_wait_ld16(s);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * ((e >> 1) & 1 ? al1 : al0));
+    tmem_st_frag4(col + x, s);
+  }
+}
+
+// What a softmax thread holds of its four fragment rows: row 8 r + g of the warp's 32, r = 0 .. 3.
+struct RowState {
+  float c[4], l[4];
+  int E[4];
+  uint32_t none;  // bit r: the row has seen nothing yet
+};
+struct TileOf {
+  uint32_t cols, col_o;  // TMEM columns of the tile's scores and of the stream's accumulator
+  int i;                 // the tile
+  bool fresh;            // the accumulator holds nothing yet
+  long long wait_limit;
+  DeviceStatus* status;
+};
+// Softmax of half HV of a tile's rows, the thread's rows 2 HV and 2 HV + 1: scores -> weights over them in TMEM.  `seen` (a
+// masked tile): bit 16 q + 2 n + e: its row 2 HV + q sees key 8 n + 2 c4 + e.  Ea, Eb: E of the rows from here on.
+template <int D, bool MASKED, int HV>
+__device__ __forceinline__ bool half(SmemT<D>& sm, RowState& st, const float (&fr)[4], const TileOf& at, uint32_t seen,
+                                     int Ea, int Eb) {
+  constexpr int r0 = 2 * HV;
+  const int slot = at.i & (kScales - 1), c4 = threadIdx.x & 3;
+  const float* ks = sm.scale[slot][0] + 2 * c4;
+  const float* vs = (MASKED ? sm.scale[slot][1] : sm.vd[slot]) + 2 * c4;
+  auto sees = [&](int q, int n, int e) { return !MASKED || ((seen >> (16 * q + 2 * n + e)) & 1u); };
+  const uint32_t cols = at.cols + HV * kLane16;
+  // c is set until a row has seen something, with E, and where a thread's sum of a tile's p passes what FP16 holds (so
+  // that it holds each weight); the half is then done again
+  bool raise = __any_sync(0xffffffffu, Ea != st.E[r0] || Eb != st.E[r0 + 1] || ((st.none >> r0) & 3u));
+  uint32_t p[16];
+  uint64_t sum[2];
+  for (;;) {
+    uint32_t s[16];
+    if (raise) {
+      const Offsets to = set_offsets(cols, ks, sm.lv[slot] + 2 * c4, MASKED ? seen : ~0u, (st.none >> r0) & 3u, fr[r0],
+                                     fr[r0 + 1], {{st.c[r0], st.c[r0 + 1]}, {st.l[r0], st.l[r0 + 1]}, {}, 0}, st.E[r0],
+                                     st.E[r0 + 1], Ea, Eb);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        st.c[r0 + q] = to.c[q];
+        st.l[r0 + q] = to.l[q];
+      }
+      st.none &= ~(to.found << r0);
+      st.E[r0] = Ea;
+      st.E[r0 + 1] = Eb;
+      if (!at.fresh && __any_sync(0xffffffffu, to.al[0] != 1.0f || to.al[1] != 1.0f)) {
+        // the stream's PV before is done first, then the accumulator's rows are multiplied
+        if (!__all_sync(0xffffffffu, wait_bounded(&sm.o_done[(at.i - 2) % kSBufs], ((at.i - 2) / kSBufs) & 1u,
+                                                  &sm.abort_flag, at.status, 103, at.wait_limit)))
+          return false;
+        tc_fence_after();
+        multiply_rows<D>(at.col_o + HV * kLane16, to.al[0], to.al[1]);
+      }
+    }
+    sum[0] = sum[1] = 0;
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb) {
+      tmem_ld_frag4(cols + 32 * cb, s);
+      tmem_wait_ld16(s);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int n = 4 * cb + m;
+        const uint64_t kk = *reinterpret_cast<const uint64_t*>(ks + 8 * n), vv = *reinterpret_cast<const uint64_t*>(vs + 8 * n);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int r = r0 + q;
+          const float2 x = unpair(mul2(pair(__uint_as_float(s[4 * m + 2 * q]), __uint_as_float(s[4 * m + 2 * q + 1])), kk));
+          float2 y = make_float2(fmaf(x.x, fr[r], -st.c[r]), fmaf(x.y, fr[r], -st.c[r]));
+          uint64_t v = vv;
+          if (MASKED) {
+            const float2 vm = unpair(v);
+            const float down = __int_as_float((127 - st.E[r]) << 23);
+            if (!sees(q, n, 0)) y.x = -INFINITY;
+            if (!sees(q, n, 1)) y.y = -INFINITY;
+            v = pair(sees(q, n, 0) ? vm.x * down : 0.0f, sees(q, n, 1) ? vm.y * down : 0.0f);
+          }
+          const uint64_t w = pair(ex2(y.x), ex2(y.y));
+          sum[q] = add2(sum[q], w);
+          const float2 z = unpair(mul2(w, v));
+          p[2 * n + q] = pack_f16x2(z.x, z.y);
+        }
+      }
+    }
+    if (raise) break;
+    const float2 y0 = unpair(sum[0]), y1 = unpair(sum[1]);
+    raise = __any_sync(0xffffffffu, !(y0.x + y0.y <= 65504.0f) || !(y1.x + y1.y <= 65504.0f));
+    if (!raise) break;
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float2 y = unpair(sum[q]);
+    st.l[r0 + q] += y.x + y.y;
+  }
+  tmem_st_half8(cols, p);
+  return true;
+}
+
+// A tile that not every row sees whole: the drafted tokens, a unit's end, a page left out.  What it takes and returns is one
+// block by value: with references the same instructions lay so that warps waited for instructions 2.5 times as long
+// (1.33 against 0.53 stalls per issue) and 21 drafted tokens over 16 contexts of 500..16384 took 212 us instead of 183.
+template <int D>
+struct MaskedRows {
+  SmemT<D>* sm;
+  const CacheAttnArgs* a;
+  TileOf at;
+  RowState st;
+  float fr[4];
+  int b, row0, rows, ctx, cnt, wrow;
+  int64_t slot0;  // the tile's first slot
+  int flags;
+  bool ok;
+};
+template <int D>
+__device__ __forceinline__ MaskedRows<D> masked_tile(MaskedRows<D> t) {
+  SmemT<D>& sm = *t.sm;
+  const CacheAttnArgs& a = *t.a;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3, slot = t.at.i & (kScales - 1);
+  const int64_t d0 = t.slot0 - t.ctx;  // drafted token of the tile's first key (below 0: context)
+  const bool drafts = d0 < t.cnt && d0 > -kTileT;
+  const int lo = (int)max(d0, (int64_t)0), hi = drafts ? min((int)(d0 + kTileT), t.cnt) : lo;  // drafted tokens [lo, hi)
+  const int words = (a.T + 31) / 32, w0 = lo / 32, sh = lo % 32;
+  uint32_t m[4][3];  // the t.rows' mask words of lo and behind, all loads before the first use
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int rw = t.wrow + g + 8 * r, tok = (t.row0 + rw) / a.G;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+      m[r][w] = a.mask && drafts && rw < t.rows && w0 + w < words ? a.mask[((int64_t)t.b * a.T + tok) * words + w0 + w] : 0u;
+  }
+  uint32_t mine[2] = {0, 0};
+  int E_new[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    uint64_t seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
+    if (t.wrow + g + 8 * r < t.rows && drafts) {
+      const int tok = (t.row0 + t.wrow + g + 8 * r) / a.G;
+      uint64_t bits = 0;  // of tokens lo, lo + 1, ...
+      if (a.mask) {
+        bits = (uint64_t)__funnelshift_r(m[r][1], m[r][2], sh) << 32 | __funnelshift_r(m[r][0], m[r][1], sh);
+      } else if (tok >= lo) {
+        bits = tok - lo >= 63 ? ~0ull : (2ull << (tok - lo)) - 1;
+      }
+      if (hi - lo < 64) bits &= (1ull << (hi - lo)) - 1;
+      seen |= bits << (lo - (int)d0);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (!((t.flags >> x) & 1)) seen &= ~(0xFFFFull << (16 * x));
+    float vm = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const uint32_t two = (uint32_t)(seen >> (8 * n + 2 * c4)) & 3u;
+      const float2 v = *reinterpret_cast<const float2*>(sm.scale[slot][1] + 8 * n + 2 * c4);
+      if (two & 1) vm = fmaxf(vm, v.x);
+      if (two & 2) vm = fmaxf(vm, v.y);
+      mine[r >> 1] |= two << (16 * (r & 1) + 2 * n);
+    }
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+    E_new[r] = max(t.st.E[r], v_exponent(__float_as_uint(vm)));
+  }
+  t.ok = half<D, true, 0>(sm, t.st, t.fr, t.at, mine[0], E_new[0], E_new[1]) &&
+         half<D, true, 1>(sm, t.st, t.fr, t.at, mine[1], E_new[2], E_new[3]);
+  return t;
+}
+
 template <int D, int KF, int VF>
 __global__ void __launch_bounds__(kThreadsT, 1)
     cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const CacheAttnArgs a) {
+                         const __grid_constant__ CacheAttnArgs a) {
   constexpr int NR = SmemT<D>::kRaw, DH = D / 2, BLK = kTileT * 128;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SmemT<D>& sm = *reinterpret_cast<SmemT<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -296,121 +538,16 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         mbar_arrive(&sm.q_full);
       }
       // From here on a thread works on its four fragment rows: row 8 r + g of the warp's 32, r = 0 .. 3.
-      float fr[4], c[4], l[4];
-      int E[4];
-      uint32_t none = 15;  // bit r: the row has seen nothing yet
+      float fr[4];
+      RowState st_rows;
+      st_rows.none = 15;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         fr[r] = __shfl_sync(0xffffffffu, f, g + 8 * r);
-        c[r] = l[r] = 0.0f;
-        E[r] = -126;
+        st_rows.c[r] = st_rows.l[r] = 0.0f;
+        st_rows.E[r] = -126;
       }
       bool fresh = true;  // no PV of this unit yet: the accumulator holds nothing
-
-      // Half `hv` of tile i's rows: the thread's rows 2 hv and 2 hv + 1.  `seen` (a masked tile): bit 16 q + 2 n + e: its
-      // row 2 hv + q sees key 8 n + 2 c4 + e.
-      auto half = [&](auto masked_tag, auto hv_tag, uint32_t cols, int i, uint32_t seen, int Ea, int Eb) {
-        constexpr bool MASKED = decltype(masked_tag)::value;
-        constexpr int hv = decltype(hv_tag)::value;
-        const int slot = i & (kScales - 1);
-        const float* ks = sm.scale[slot][0] + 2 * c4;
-        const float* vs = (MASKED ? sm.scale[slot][1] : sm.vd[slot]) + 2 * c4;
-        auto sees = [&](int q, int n, int e) { return !MASKED || ((seen >> (16 * q + 2 * n + e)) & 1u); };
-        const int E_new[2] = {Ea, Eb};
-        cols += hv * kLane16;
-        // c is raised until a row has seen something, with E, and where a thread's sum of a tile's p passes 2^14 (so that
-        // FP16 holds each of them); the half is then done again
-        bool raise = MASKED || __any_sync(0xffffffffu, ((none >> (2 * hv)) & 3u) || Ea != E[2 * hv]);
-        uint32_t p[16];
-        uint64_t sum[2];
-        for (;;) {
-          uint32_t s[16];
-          if (raise) {
-            float top[2] = {-INFINITY, -INFINITY}, al_o[2];
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb) {
-              tmem_ld_frag4(cols + 32 * cb, s);
-              tmem_wait_ld16(s);
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const float2 kk = *reinterpret_cast<const float2*>(ks + 8 * (4 * cb + m));
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (sees(e >> 1, 4 * cb + m, e & 1))
-                    top[e >> 1] = fmaxf(top[e >> 1], __uint_as_float(s[4 * m + e]) * ((e & 1) ? kk.y : kk.x));
-              }
-            }
-            bool moved = false;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int r = 2 * hv + q;
-              top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 1));
-              top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], 2));
-              const bool nothing = (none >> r) & 1u;
-              const float c_new = nothing ? (top[q] == -INFINITY ? 0.0f : top[q] * fr[r]) : fmaxf(c[r], top[q] * fr[r]);
-              const float al = nothing ? 0.0f : ex2(c[r] - c_new);
-              al_o[q] = E_new[q] == E[r] ? al : al * ex2((float)(E[r] - E_new[q]));
-              moved |= al_o[q] != 1.0f;
-              if (top[q] != -INFINITY) none &= ~(1u << r);
-              c[r] = c_new;
-              E[r] = E_new[q];
-              l[r] *= al;
-            }
-            if (!fresh && __any_sync(0xffffffffu, moved)) {
-              // the stream's PV before is done first, then the accumulator's rows are multiplied
-              if (!(ok = wait(&sm.o_done[(i - 2) % kSBufs], (i - 2) / kSBufs, 3))) return;
-              tc_fence_after();
-#pragma unroll 1
-              for (int x = 0; x < D; x += 32) {
-                tmem_ld_frag4(col_o + hv * kLane16 + x, s);
-                tmem_wait_ld16(s);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * al_o[(e >> 1) & 1]);
-                tmem_st_frag4(col_o + hv * kLane16 + x, s);
-              }
-            }
-          }
-          sum[0] = sum[1] = 0;
-#pragma unroll
-          for (int cb = 0; cb < 2; ++cb) {
-            tmem_ld_frag4(cols + 32 * cb, s);
-            tmem_wait_ld16(s);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int n = 4 * cb + m;
-              const uint64_t kk = *reinterpret_cast<const uint64_t*>(ks + 8 * n), vv = *reinterpret_cast<const uint64_t*>(vs + 8 * n);
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int r = 2 * hv + q;
-                const float2 x = unpair(mul2(pair(__uint_as_float(s[4 * m + 2 * q]), __uint_as_float(s[4 * m + 2 * q + 1])), kk));
-                float2 y = make_float2(fmaf(x.x, fr[r], -c[r]), fmaf(x.y, fr[r], -c[r]));
-                uint64_t v = vv;
-                if (MASKED) {
-                  const float2 vm = unpair(v);
-                  const float down = __int_as_float((127 - E[r]) << 23);
-                  if (!sees(q, n, 0)) y.x = -INFINITY;
-                  if (!sees(q, n, 1)) y.y = -INFINITY;
-                  v = pair(sees(q, n, 0) ? vm.x * down : 0.0f, sees(q, n, 1) ? vm.y * down : 0.0f);
-                }
-                const uint64_t w = pair(ex2(y.x), ex2(y.y));
-                sum[q] = add2(sum[q], w);
-                const float2 z = unpair(mul2(w, v));
-                p[2 * n + q] = pack_f16x2(z.x, z.y);
-              }
-            }
-          }
-          if (raise) break;
-          const float2 y0 = unpair(sum[0]), y1 = unpair(sum[1]);
-          raise = __any_sync(0xffffffffu, !(y0.x + y0.y <= 16384.0f) || !(y1.x + y1.y <= 16384.0f));
-          if (!raise) break;
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float2 y = unpair(sum[q]);
-          l[2 * hv + q] += y.x + y.y;
-        }
-        tmem_st_half8(cols, p);
-      };
 
       // ---- tiles of this stream
       int i = (int)(seg - st.s);
@@ -422,59 +559,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const uint32_t cols = lanes + buf * 64;
         if (!idle) {
           const int flags = sm.flags[slot];
+          const TileOf at_tile{cols, col_o, i, fresh, a.wait_limit, status};
           if (!(flags & kMasked)) {
             const int E_new = sm.e[slot];
-            half(std::false_type{}, std::integral_constant<int, 0>{}, cols, i, ~0u, E_new, E_new);
-            if (ok) half(std::false_type{}, std::integral_constant<int, 1>{}, cols, i, ~0u, E_new, E_new);
+            ok = half<D, false, 0>(sm, st_rows, fr, at_tile, ~0u, E_new, E_new) &&
+                 half<D, false, 1>(sm, st_rows, fr, at_tile, ~0u, E_new, E_new);
           } else {
-            const int64_t slot0 = (int64_t)(st.s + i - u.start) * kTileT;
-            const int64_t d0 = slot0 - ctx;  // drafted token of the tile's first key (below 0: context)
-            const bool drafts = d0 < cnt && d0 > -kTileT;
-            const int lo = (int)max(d0, (int64_t)0), hi = drafts ? min((int)(d0 + kTileT), cnt) : lo;  // drafted tokens [lo, hi)
-            const int words = (a.T + 31) / 32, w0 = lo / 32, sh = lo % 32;
-            uint32_t m[4][3];  // the rows' mask words of lo and behind, all loads before the first use
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int rw = wrow + g + 8 * r, t = (row0 + rw) / a.G;
-#pragma unroll
-              for (int w = 0; w < 3; ++w)
-                m[r][w] = a.mask && drafts && rw < rows && w0 + w < words
-                              ? a.mask[((int64_t)b * a.T + t) * words + w0 + w] : 0u;
-            }
-            uint32_t mine[2] = {0, 0};
-            int E_new[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              uint64_t seen = d0 <= -64 ? ~0ull : d0 >= 0 ? 0ull : ~0ull >> (64 + d0);
-              if (wrow + g + 8 * r < rows && drafts) {
-                const int t = (row0 + wrow + g + 8 * r) / a.G;
-                uint64_t bits = 0;  // of tokens lo, lo + 1, ...
-                if (a.mask) {
-                  bits = (uint64_t)__funnelshift_r(m[r][1], m[r][2], sh) << 32 | __funnelshift_r(m[r][0], m[r][1], sh);
-                } else if (t >= lo) {
-                  bits = t - lo >= 63 ? ~0ull : (2ull << (t - lo)) - 1;
-                }
-                if (hi - lo < 64) bits &= (1ull << (hi - lo)) - 1;
-                seen |= bits << (lo - (int)d0);
-              }
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (!((flags >> x) & 1)) seen &= ~(0xFFFFull << (16 * x));
-              float vm = 0.0f;
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                const uint32_t two = (uint32_t)(seen >> (8 * n + 2 * c4)) & 3u;
-                const float2 v = *reinterpret_cast<const float2*>(sm.scale[slot][1] + 8 * n + 2 * c4);
-                if (two & 1) vm = fmaxf(vm, v.x);
-                if (two & 2) vm = fmaxf(vm, v.y);
-                mine[r >> 1] |= two << (16 * (r & 1) + 2 * n);
-              }
-              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-              E_new[r] = max(E[r], v_exponent(__float_as_uint(vm)));
-            }
-            half(std::true_type{}, std::integral_constant<int, 0>{}, cols, i, mine[0], E_new[0], E_new[1]);
-            if (ok) half(std::true_type{}, std::integral_constant<int, 1>{}, cols, i, mine[1], E_new[2], E_new[3]);
+            MaskedRows<D> m{&sm, &a, at_tile, st_rows, {fr[0], fr[1], fr[2], fr[3]}, b, row0, rows, ctx, cnt, wrow,
+                            (int64_t)(st.s + i - u.start) * kTileT, flags, true};
+            m = masked_tile<D>(m);
+            st_rows = m.st;
+            ok = m.ok;
           }
           if (!ok) break;
           tmem_wait_st();
@@ -494,14 +589,16 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float x = l[r];
+        float x = st_rows.l[r];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         if (c4 == 0) {
           const int rw = wrow + g + 8 * r;
-          sm.l[sid][rw] = x;
-          sm.c[sid][rw] = (none >> r) & 1 ? -INFINITY : c[r];
-          sm.up[sid][rw] = fresh ? 0.0f : __int_as_float((127 + E[r]) << 23);  // 2^E; 0: the accumulator holds nothing
+          const Mass m = normalised((st_rows.none >> r) & 1 ? -INFINITY : st_rows.c[r], x);
+          sm.l[sid][rw] = m.l;
+          sm.c[sid][rw] = m.c;
+          sm.g[sid][rw] = m.g;
+          sm.up[sid][rw] = fresh ? 0.0f : __int_as_float((127 + st_rows.E[r]) << 23);  // 2^E; 0: the accumulator holds nothing
         }
       }
       tc_fence_before();
@@ -512,6 +609,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const float ca = sm.c[0][row], cb = sm.c[1][row], cm = fmaxf(ca, cb);
         const float wa = ca == -INFINITY ? 0.0f : ex2(ca - cm), wb = cb == -INFINITY ? 0.0f : ex2(cb - cm);
         const float lt = sm.l[0][row] * wa + sm.l[1][row] * wb;
+        const float ga = sm.g[0][row], gb = sm.g[1][row];
         const bool has_a = sm.up[0][row] != 0.0f, has_b = sm.up[1][row] != 0.0f;
         const bool whole = seg == u.start && seg_end == unit_end, on = row < rows;
         const float inv = whole ? row_inverse(lt) : 1.0f;
@@ -529,7 +627,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           float o[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            o[e] = (has_a ? __uint_as_float(oa[e]) * fa : 0.0f) + (has_b ? __uint_as_float(ob[e]) * fb : 0.0f);
+            o[e] = (has_a ? __uint_as_float(oa[e]) * ga * fa : 0.0f) + (has_b ? __uint_as_float(ob[e]) * gb * fb : 0.0f);
           if (on && whole) {
 #pragma unroll
             for (int e = 0; e < 16; e += 8)
@@ -559,7 +657,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     // warps of K and of V, each at its own pace
     const bool is_v = warp >= kConvV;
     const int w = warp - (is_v ? kConvV : kConvK);
-    int E = -126;  // of the tiles so far that every row sees whole
+    int E = -126;  // of the unit's tiles so far; behind one with a draft or an end none follows that needs it
     for (int i = 0; i < n_tiles; ++i) {
       const int r = i % NR, slot = i & (kScales - 1);
       if (!wait(&sm.raw_full[r], i / NR, 6)) break;
@@ -573,14 +671,20 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           sm.scale[slot][0][lane + 32] *= a.sl2;
         } else if (w == 0) {
           if (flags & kFirst) E = -126;
+          float v0 = sm.scale[slot][1][lane], v1 = sm.scale[slot][1][lane + 32];
+          if (!((flags >> (lane / 16)) & 1)) v0 = 0.0f;  // a group without keys: what the slot held before
+          if (!((flags >> (2 + lane / 16)) & 1)) v1 = 0.0f;
+          // with the tiles that have a page left out in the middle of a context, whose E the rows took for themselves
+          E = max(E, v_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(v0, v1), 0.0f)))));
           if (!(flags & kMasked)) {
-            const float v0 = sm.scale[slot][1][lane], v1 = sm.scale[slot][1][lane + 32];
-            E = max(E, v_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(v0, v1), 0.0f)))));
             const float down = __int_as_float((127 - E) << 23);
             sm.vd[slot][lane] = v0 * down;
             sm.vd[slot][lane + 32] = v1 * down;
             if (lane == 0) sm.e[slot] = E;
           }
+        } else if (w == 2) {
+          sm.lv[slot][lane] = lg2f(sm.scale[slot][1][lane]);
+          sm.lv[slot][lane + 32] = lg2f(sm.scale[slot][1][lane + 32]);
         }
         if (!wait(&sm.k_empty[i % kKStages], (i / kKStages) ^ 1, 7)) break;
         convert<D, KF>(smem_u32(sm.raw[r][0]), smem_u32(sm.k[i % kKStages]), w, lane, false);

@@ -91,7 +91,40 @@ __device__ __forceinline__ int q_exponent(uint32_t top) {
 // kept what rounding had taken from c, which passes 2^16 from scores of 2^40 on.
 __device__ __forceinline__ float q_factor(int eq) { return __int_as_float((127 + eq) << 23); }
 
-constexpr float kRaise = 8.0f;  // a row's offset is raised for scores that pass it by more (log2)
+// A row's weights p v-scale 2^-E are FP16 in the MMAs, which holds 11 bits from 2^-14 to 2^16 and ever fewer down to 2^-25.
+// Where that range lies is what the row's offset c decides: p = 2^(s - c), V scales times 2^-E are at most 1, and c follows
+// the largest weight, not the largest score: a key of nearly all the probability and next to no value, or of a huge
+// V scale and no probability, leaves the others their bits.  Weights down to 2^-21 of the largest that the row met keep
+// 11 bits; the others are off by at most 2^-32 of the largest.  p itself is FP32 and may be large.
+constexpr float kHead = 8.0f;   // when c is set, the tile's largest weight is in (2^(kHead - 1), 2^kHead]
+constexpr float kLimit = 15.0f;  // scores that pass c by more raise it (log2)
+constexpr float kLow = 88.0f;    // p stays at or below 2^(kLow + kHead), however small the weights beside it are
+constexpr float kMass = 100.0f;  // a row's sum stays below 2^kMass when c is lowered because E grew
+
+// c for a tile whose largest score is `top` and whose largest score plus log2 of its V scale is `weight` (rounded up): an
+// integer, so that factors between offsets are powers of two; rounded up, so that large scores, which leave no room
+// for the small terms, put c at `top` at most.
+__device__ __forceinline__ float tile_offset(float top, float weight, int E) {
+  return ceilf(__fadd_ru(fminf(fmaxf(__fadd_ru(weight, -(float)E), __fadd_ru(top, -kLow)), top), -kHead));
+}
+// c when E grows by `de`: what keeps the unit of the weights' sums, 2^(c + E), as long as the row's sum, `mass` so far, has room.
+__device__ __forceinline__ float kept_offset(float c, int de, float mass) {
+  const float room = fmaxf(kMass - (float)((__float_as_int(mass) >> 23) - 126), 0.0f);
+  return __fadd_ru(c, -fminf((float)de, room));
+}
+
+// A row's sum l with its offset c as c' and l' in [1, 2), and g = l' / l: where l may be large, 2^E l is not.
+struct Mass {
+  float c, l, g;
+};
+__device__ __forceinline__ Mass normalised(float c, float l) {
+  const int k = l > 0.0f && l < 0x1p127f ? (__float_as_int(l) >> 23) - 127 : 0;  // zero, infinity and NaN stay
+  if (k == 0) return {c, l, 1.0f};
+  const float c2 = c + (float)k;  // rounded where c passes 2^24: the factor is of what it became
+  float g;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(c - c2));
+  return {c2, l * g, g};
+}
 
 }  // namespace cattn
 }  // namespace sage

@@ -520,9 +520,12 @@ SAGE_API int sage_cache_read(const sage_cache* cache, const int32_t* page_table,
  *     on are left as they were and bits of j >= count[b] are ignored.
  *   - s_j = q . k_j * sm_scale (<= 0: 1/sqrt(D)) on the dequantised K, FP32
  *     softmax statistics, out = bf16(sum softmax(s)_j v_j); the products are
- *     of FP16 values, exact for the codes, with FP32 sums; a probability times
- *     its V scale over a power of two at or above the row's largest V scale is
- *     rounded to FP16.
+ *     of FP16 values, exact for the codes, with FP32 sums.  A weight, the
+ *     probability times the V scale, is rounded to FP16: to 11 bits down to
+ *     2^-21 of the row's largest weight, and off by at most 2^-32 of the largest
+ *     below that.  (The largest weight counts, not the largest probability or
+ *     V scale, unless its key is less probable than another by over 2^88.)
+ *     Scores may have any size that FP32 holds, for K below 2^96 in magnitude.
  *   - lse (NULL or [B][T][Hq]): ln sum_j exp(s_j).
  *   - A row that sees nothing: out 0, lse -inf.
  * Masked and unused slots may hold any bytes.  out and lse must not overlap the
