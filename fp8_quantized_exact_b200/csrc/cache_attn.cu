@@ -221,7 +221,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int eq = q_exponent(top);
-      const float down = __int_as_float((127 - eq) << 23);
+      const float down = q_down(top, eq);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const uint32_t w0 = w[2 * s], w1 = w[2 * s + 1];

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         if (!(ok = wait(&sm.swap, swaps++, 0))) break;
         top = max(top, sm.amax[sid ^ 1][row]);
         const int eq = q_exponent(top);
-        const float down = __int_as_float((127 - eq) << 23);
+        const float down = q_down(top, eq);
         f = q_factor(eq);
 #pragma unroll
         for (int x0 = 0; x0 < DH / 8; x0 += 4) {

@@ -86,6 +86,11 @@ __device__ __forceinline__ uint32_t swizzled(int key, int chunk) {
 __device__ __forceinline__ int q_exponent(uint32_t top) {
   return (top == 0 || top >= 0x7F80u) ? 0 : max((int)(top >> 7) - 127 - 13, -110);
 }
+// 2^-eq, by which a Q row is multiplied.  A row with an infinity or a NaN becomes NaN in every channel, so that all its scores
+// are: infinities would pass for a row that sees nothing where they all are negative.
+__device__ __forceinline__ float q_down(uint32_t top, int eq) {
+  return __int_as_float(top >= 0x7F80u ? 0x7FC00000 : (127 - eq) << 23);
+}
 // The factor of the row's scores, which hold sm_scale log2 e already (it goes to the key's scale): a power of two, so that
 // x f - c is the difference of two scores without a rounding of either product.  With sm_scale in f the fused x f - c
 // kept what rounding had taken from c, which passes 2^16 from scores of 2^40 on.

@@ -528,6 +528,8 @@ SAGE_API int sage_cache_read(const sage_cache* cache, const int32_t* page_table,
  *     Scores may have any size that FP32 holds, for K below 2^96 in magnitude.
  *   - lse (NULL or [B][T][Hq]): ln sum_j exp(s_j).
  *   - A row that sees nothing: out 0, lse -inf.
+ *   - A row whose Q has an infinity or a NaN, or that sees a token with a NaN
+ *     scale: out and lse NaN.
  * Masked and unused slots may hold any bytes.  out and lse must not overlap the
  * inputs.  Workspace: sage_workspace_bytes(SAGE_OP_CACHE_ATTN, ...). */
 SAGE_API int sage_cache_attn(sage_view_bf16 q, const sage_cache* cache, const int32_t* page_table, int table_pages,

@@ -163,3 +163,44 @@ def test_scores_that_do_not_differ_and_that_climb(sage, kind, T, G, D):
     if kind == "steps":
         s = s + torch.arange(n, dtype=torch.float64) // 32 * 0.7
     check(sage, n, T, G, D, E4M3, s, torch.ones(H, n, dtype=torch.float64), count(T, G, D, WHOLE), seed=2)
+
+
+@pytest.mark.parametrize("T,G,D", SHAPES)
+@pytest.mark.parametrize("poison", [math.inf, -math.inf, math.nan])
+def test_poison_in_q_spoils_its_row_and_no_other(sage, poison, T, G, D):
+    """An infinity or a NaN in a Q row, on a channel where all keys have one sign: every score of the row is that infinity
+    or NaN, and so the row is NaN, also where all are -infinity; a row that sees nothing stays 0 and -infinity, and the
+    other rows keep their bits."""
+    B, H, n, page = 2, 2, 150, 16
+    g = torch.Generator().manual_seed(T + D)
+    context = torch.tensor([n, 0], dtype=torch.int32, device=DEV)
+    pages = -(-(n + T) // page)
+    cache = sage.cache_buffers(B * pages, H, page, D)
+    table = torch.arange(B * pages, dtype=torch.int32, device=DEV).view(B, pages)
+    x = torch.randn(B, n + T, H, D, generator=g)
+    x[..., 3] = x[..., 3].abs() + 0.1
+    ws = sage.workspace(sage.SAGE_OP_CACHE_ATTN, 1, 1, 1, D)
+    sage.sage_cache_append(cache, x.bfloat16().to(DEV), x.bfloat16().to(DEV), table, None, None, ws)
+    q = torch.randn(B, T, H * G, D, generator=g).bfloat16().to(DEV)
+    mask = torch.zeros(B, T, -(-T // 32), dtype=torch.int32, device=DEV)
+    mask[:, 1:, 0] = 1  # the rows of token 0 of the second sequence see nothing, the others the first drafted token
+
+    def run(q):
+        out, lse = torch.full_like(q, 5.0), torch.full((B, T, H * G), 5.0, device=DEV)
+        sage.sage_cache_attn(q, cache, table, context, None, mask, out, lse, 0.0, ws)
+        torch.cuda.synchronize()
+        assert sage.sage_read_device_status(ws) == sage.SAGE_OK
+        return out, lse
+
+    want, wl = run(q)
+    assert torch.isfinite(want).all() and (want[1, 0] == 0).all() and (wl[1, 0] == -math.inf).all()
+    bad = q.clone()
+    spoiled = torch.zeros(B, T, H * G, dtype=torch.bool, device=DEV)
+    for t, h in ((0, 0), (T - 1, 1), (T // 2, H * G - 1)):
+        bad[:, t, h, 3] = poison
+        spoiled[:, t, h] = True
+    spoiled[1, 0] = False
+    out, lse = run(bad)
+    assert torch.isnan(out[spoiled]).all() and torch.isnan(lse[spoiled]).all()
+    assert torch.equal(out[~spoiled].view(torch.int16), want[~spoiled].view(torch.int16))
+    assert torch.equal(lse[~spoiled], wl[~spoiled])
