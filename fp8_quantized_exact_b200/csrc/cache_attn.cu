@@ -123,6 +123,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
           (long long)ctx + cnt > ((long long)a.c.table_pages << a.c.page_shift))
         flag_bad(a.c.status, kWhereAttn);
     }
+  if (threadIdx.x == 0) cut_unit(a, blockIdx.x)->parts = 0;  // behind the wait: the join of a call before may read its own until then
   if (st.s >= st.e) return;
 
   // ---- this warp's tiles: list indices [first, last)
@@ -562,6 +563,8 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
       float* to = part_of<R, D>(a, blockIdx.x, cut.start < st.s ? 0 : 1);
       *reinterpret_cast<float4*>(to + r * D + col) = o;
       if (col == 0) { to[R * D + r] = c; to[R * D + R + r] = l; }
+      if (col == 0 && r == 0 && cut.start >= st.s)
+        *cut_unit(a, blockIdx.x) = CutUnit{(int)((cut.end - 1) / st.share - blockIdx.x) + 1, cut.b, cut.h, cut.row0, cut.rows};
     }
   }
 }
@@ -599,7 +602,7 @@ int by_rows(const CacheAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t cache_attn_workspace_bytes() { return kPartBytes; }
+size_t cache_attn_workspace_bytes() { return kPartBytes + kCutBytes; }
 
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   // The tcgen05 variant takes 128 rows at once at nearly the time of 16; this one reads and converts the cache again for

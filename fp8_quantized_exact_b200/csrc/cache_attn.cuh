@@ -151,6 +151,18 @@ constexpr int kMaxCtas = 148;  // one per SM
 constexpr int kMaxRows = 128;  // of a unit
 constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (kMaxRows * 128 + 2 * kMaxRows) * sizeof(float);
 
+// What the join needs of the unit that begins in a CTA's stretch and goes on behind it; parts 0: there is none.  The main
+// kernel leaves one for each CTA behind its parts in the workspace: what the lengths were is known to it alone, since the join
+// starts before it may read what was written in front of the main kernel.
+struct alignas(16) CutUnit {
+  int parts, b, h, row0, rows;
+};
+constexpr size_t kCutBytes = kMaxCtas * sizeof(CutUnit);
+static_assert(kPartBytes % alignof(CutUnit) == 0, "the records lie behind the parts");
+__device__ __forceinline__ CutUnit* cut_unit(const CacheAttnArgs& a, int cta) {
+  return reinterpret_cast<CutUnit*>(static_cast<char*>(a.workspace) + kPartBytes) + cta;
+}
+
 // Parts in the workspace: [2 * CTA + slot] of R x D sums, R offsets, R denominators.
 template <int R, int D>
 __device__ __forceinline__ float* part_of(const CacheAttnArgs& a, int cta, int slot) {
@@ -195,8 +207,8 @@ __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, int b, int h, 
 
 // Joins the parts of the unit that begins in CTA blockIdx.x's stretch and is
 // cut by its end; blockIdx.y takes kRows of its rows.  Threads beyond a float4 of each share the
-// parts, group by group in list order, so the sums have one order.  The
-// blocks find their unit while the CTAs of the main kernel end, and wait for them.
+// parts, group by group in list order, so the sums have one order.  The blocks
+// become resident while the CTAs of the main kernel end, and read nothing before those have.
 template <int R, int D>
 struct Join {
   // few rows: more threads for each, since one unit may have a part in every CTA; many: a grid that stays within a
@@ -204,28 +216,18 @@ struct Join {
   static constexpr int kRows = R >= 64 ? 8 : 4, kThreads = 256, kItems = kRows * D / 4, kGroups = kThreads / kItems;
   static_assert(kThreads % kItems == 0 && R % kRows == 0, "whole groups and blocks");
 };
-template <int TILE, int R, int D, int STEP>
-__global__ void __launch_bounds__(256) cache_attn_join_kernel(const CacheAttnArgs a, int ctas) {
+template <int R, int D>
+__global__ void __launch_bounds__(256) cache_attn_join_kernel(const CacheAttnArgs a) {
   using J = Join<R, D>;
   constexpr int RB = J::kRows, V4 = D / 4;
   __shared__ float c_s[RB][kMaxCtas], l_s[RB][kMaxCtas];  // offsets, then weights; denominators
   __shared__ float c_row[RB], l_row[RB];
   __shared__ float4 o_s[J::kGroups > 1 ? J::kThreads : 1];
-  // the lengths are older than the kernel in front, which waited for them
-  const Stretch st = find_stretch<TILE, R, STEP>(a, blockIdx.x, ctas);
-  Place p;
-  Unit u;
-  unsigned end = 0;
-  if (st.s < st.e) {
-    p = place_of<TILE, R>(a, st.own, st.e - 1);
-    u = unit_of(p, st.e - 1);
-    end = u.start + p.s.n;
-  }
   begin_dependent();
-  if (st.s >= st.e || u.start < st.s || end <= st.e) return;
-  const int first = blockIdx.x, np = (int)((end - 1) / st.share) - first + 1;
-  const int r0 = blockIdx.y * RB, nr = min(RB, min(R, p.s.cnt * a.G - u.rt * R) - r0);
-  if (nr <= 0) return;
+  const int first = blockIdx.x, r0 = blockIdx.y * RB;
+  const CutUnit u = *cut_unit(a, first);
+  const int np = u.parts, nr = min(RB, u.rows - r0);
+  if (np == 0 || nr <= 0) return;
   auto part = [&](int i) { return part_of<R, D>(a, first + i, i == 0 ? 1 : 0); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < np * RB; i += J::kThreads) {
@@ -276,8 +278,8 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const CacheAttnArg
     }
   }
   if (r >= nr) return;
-  store_out(a, p.b, u.h, u.rt * R + r0 + r, col, o, row_inverse(l_row[r]));
-  if (col == 0) store_lse(a, p.b, u.h, u.rt * R + r0 + r, c_row[r], l_row[r]);
+  store_out(a, u.b, u.h, u.row0 + r0 + r, col, o, row_inverse(l_row[r]));
+  if (col == 0) store_lse(a, u.b, u.h, u.row0 + r0 + r, c_row[r], l_row[r]);
 }
 
 template <int TILE, int R, int D, int STEP>
@@ -285,8 +287,7 @@ int launch_join(const CacheAttnArgs& a, cudaStream_t s) {
   using J = Join<R, D>;
   const int rows = min(R, a.T * a.G);                                                // of the fullest unit
   const int ctas = (int)fmin(kMaxCtas, ceil(longest_list<TILE, R>(a) / STEP));  // that can have a stretch
-  return launch_dependent(cache_attn_join_kernel<TILE, R, D, STEP>, dim3(ctas, (rows + J::kRows - 1) / J::kRows),
-                          J::kThreads, 0, s, a, kMaxCtas);
+  return launch_dependent(cache_attn_join_kernel<R, D>, dim3(ctas, (rows + J::kRows - 1) / J::kRows), J::kThreads, 0, s, a);
 }
 
 }  // namespace cattn

@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           (long long)ctx + cnt > ((long long)a.c.table_pages << a.c.page_shift))
         flag_bad(status, kWhereAttn);
     }
+  if (threadIdx.x == 0) cut_unit(a, blockIdx.x)->parts = 0;  // behind the wait: the join of a call before may read its own until then
   if (st.s >= st.e) return;
   if (warp == kQkWarpT) tmem_alloc(&sm.tmem_base, kColsT);
   tc_fence_before();
@@ -646,6 +647,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           } else {
             part[kRowsT * D + row] = cm;
             part[kRowsT * D + kRowsT + row] = lt;
+            if (row == 0 && seg == u.start)
+              *cut_unit(a, blockIdx.x) = CutUnit{(int)((unit_end - 1) / st.share - blockIdx.x) + 1, b, h, row0, rows};
           }
         }
       }

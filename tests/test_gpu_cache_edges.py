@@ -1,0 +1,72 @@
+"""The serving calls where their inputs change under way: lengths written right in front of a call, forks of streams, and
+the append's largest values."""
+import pytest
+
+import cache_util as cu
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+INT8, E4M3 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def sage():
+    import fp8_quantized_exact_b200 as s
+    from fp8_quantized_exact_b200 import build
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    return s
+
+
+def problem(sage, B, T, G, H, D, n, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    page = 64
+    per = -(-(n + T) // page)
+    cache = sage.cache_buffers(B * per, H, page, D)
+    table = torch.randperm(B * per, device=DEV, generator=g).to(torch.int32).view(B, per).contiguous()
+    ws = sage.workspace(sage.SAGE_OP_CACHE_ATTN, 1, 1, 1, D)
+    x = torch.randn(2, B, n + T, H, D, device=DEV, generator=g).bfloat16()
+    sage.sage_cache_append(cache, x[0], x[1], table, None, None, ws)
+    q = torch.randn(B, T, H * G, D, device=DEV, generator=g).bfloat16()
+    return cache, table, ws, q
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("B,T,G,H,D", [(1, 1, 4, 8, 128), (3, 2, 8, 2, 64), (40, 1, 7, 2, 128), (5, 16, 8, 2, 128), (2, 64, 1, 1, 64)])
+def test_lengths_written_right_in_front_of_each_call(sage, B, T, G, H, D, captured):
+    """Calls whose lengths, and with them which units are cut and into how many parts, jump from one to the next, written by
+    the kernel in front: the bits of calls on an idle device."""
+    n, calls = 6000, 24
+    cache, table, ws, q = problem(sage, B, T, G, H, D, n, seed=B + T)
+    g = torch.Generator("cuda").manual_seed(7)
+    lengths = torch.randint(0, n + 1, (calls, B), device=DEV, generator=g, dtype=torch.int32)
+    lengths[::3] //= 50
+    counts = torch.randint(0, T + 1, (calls, B), device=DEV, generator=g, dtype=torch.int32)
+    ctx, cnt = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    out = torch.full((2, calls) + tuple(q.shape), 5.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((2, calls, B, T, H * G), 5.0, device=DEV)
+
+    def call(k, i):
+        torch.add(lengths[i], 0, out=ctx)
+        torch.add(counts[i], 0, out=cnt)
+        sage.sage_cache_attn(q, cache, table, ctx, cnt, None, out[k, i], lse[k, i], 0.0, ws)
+
+    for i in range(calls):
+        call(0, i)
+        torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(calls):
+                call(1, i)
+        graph.replay()
+    else:
+        for i in range(calls):
+            call(1, i)
+    torch.cuda.synchronize()
+    assert sage.sage_read_device_status(ws) == sage.SAGE_OK
+    assert torch.equal(out[0].view(torch.int16), out[1].view(torch.int16)) and torch.equal(lse[0], lse[1])
+    assert torch.isfinite(out).all()
