@@ -7,9 +7,10 @@
 // of zeros has scale 0 and codes 0; a row with an infinity or a NaN has scale
 // NaN and codes 0, so that it reads back as NaN and spoils what attends to it.
 //
-// The quotient: inv + rest is top / amax to 2^-45 (relative), and
-// t = fma(x, inv, x * rest) is q = x * top / amax rounded once to FP32, but for
-// quotients within 2^-45 of half-way between two FP32 values.  With 8
+// The quotient: inv + rest is top / amax to 2^-45 (relative) for amax below 2^112, and to less and less above,
+// where rest is subnormal: 2^-29 at the largest BF16 values.  So t = fma(x, inv, x * rest) is q = x * top / amax to less
+// than half an FP32 step before its one rounding: a q that is an FP32 value, as every half-way point between two codes
+// is, is t itself, and any other t is within 2^-23 of q.  With 8
 // significant bits in x and in amax, a q that is not half-way between two codes
 // is at least 2^-16 away from half-way (INT8: |254 xm - a (2k+1) 2^s| >= 1 over
 // a (2k+1) 2^s <= 2^16; E4M3: the denominator is at most 2^13), so t is half-way

@@ -70,3 +70,29 @@ def test_lengths_written_right_in_front_of_each_call(sage, B, T, G, H, D, captur
     assert sage.sage_read_device_status(ws) == sage.SAGE_OK
     assert torch.equal(out[0].view(torch.int16), out[1].view(torch.int16)) and torch.equal(lse[0], lse[1])
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("fmt", [INT8, E4M3])
+@pytest.mark.parametrize("power", [104, 111, 115, 119, 120])
+def test_append_ties_of_the_largest_values(sage, fmt, power):
+    """All half-way cases (BF16 values of twelve binades against every 8-bit maximum) where the quotient's second term is
+    subnormal: the codes are those of the exact quotient."""
+    D, dt = 128, (torch.int8, torch.float8_e4m3fn)[fmt]
+    mant = torch.arange(128, 256, dtype=torch.float64)
+    rows = []
+    for e in range(12):
+        body = (mant[None, 1:] * 2.0 ** -e).expand(128, 127).clone()
+        body[body > mant[:, None]] = 1.0
+        rows.append(torch.cat((mant[:, None], body * torch.where(torch.arange(127) % 2 == 0, 1.0, -1.0)), 1))
+    x = (torch.cat(rows) * 2.0 ** power).to(torch.bfloat16)[None, :, None].to(DEV)
+    assert torch.isfinite(x).all()
+    n = x.shape[1]
+    ws = sage.workspace(sage.SAGE_OP_CACHE, 1, 1, 1, D)
+    cache = sage.cache_buffers(-(-n // 64), 1, 64, D, fmt, fmt)
+    table = torch.arange(-(-n // 64), dtype=torch.int32, device=DEV)[None]
+    sage.sage_cache_append(cache, x, x, table, None, None, ws)
+    torch.cuda.synchronize()
+    assert sage.sage_read_device_status(ws) == sage.SAGE_OK
+    code, scale = cu.quantise(x[0, :, 0], dt)
+    assert torch.equal(cache[0].double().permute(0, 2, 1, 3).reshape(-1, D)[:n], code)
+    assert torch.equal(cache[1].permute(0, 2, 1).reshape(-1)[:n], scale)
