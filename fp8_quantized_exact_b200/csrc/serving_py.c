@@ -5,7 +5,9 @@
  * microseconds on the GPU.  Read from Python with ctypes, the attributes of the
  * six to ten tensors and the twenty-odd arguments took 8 to 10 us of host time
  * per call, more than the kernels.  The library stays what ctypes loaded:
- * bind() takes the addresses of its functions. */
+ * bind() takes the addresses of its functions.  They run without the interpreter
+ * lock, as through ctypes: a launch can block, and another thread may have to
+ * free it. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -257,6 +259,7 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int inverse, has_pos = a[4] != Py_None, has_k;
   double mscale;
   void* s;
+  int rc;
   (void)self;
   if (count_args(n, 11)) return NULL;
   has_k = a[1] != Py_None;
@@ -288,10 +291,13 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   layout = PyLong_AsLong(a[7]);
   inverse = PyObject_IsTrue(a[9]);
   if (PyErr_Occurred() || stream_of(&c, a[10], &s)) return NULL;
-  return done(&c, p_rope(as_view(&q), (int)q.shape[2], qo.ptr, qo.stride[0], qo.stride[1], qo.stride[2], vk,
-                         has_k ? (int)k.shape[2] : 0, ko.ptr, ko.stride[0], ko.stride[1], ko.stride[2],
-                         (const int32_t*)pos.ptr, pos.nd == 2 ? pos.stride[0] : 0, (const double*)f.ptr, (float)mscale,
-                         (int)layout, (int)rot, inverse, (int)q.shape[0], (int)q.shape[1], (int)q.shape[3], s));
+  Py_BEGIN_ALLOW_THREADS
+  rc = p_rope(as_view(&q), (int)q.shape[2], qo.ptr, qo.stride[0], qo.stride[1], qo.stride[2], vk,
+              has_k ? (int)k.shape[2] : 0, ko.ptr, ko.stride[0], ko.stride[1], ko.stride[2],
+              (const int32_t*)pos.ptr, pos.nd == 2 ? pos.stride[0] : 0, (const double*)f.ptr, (float)mscale,
+              (int)layout, (int)rot, inverse, (int)q.shape[0], (int)q.shape[1], (int)q.shape[3], s);
+  Py_END_ALLOW_THREADS
+  return done(&c, rc);
 }
 
 /* append(cache, k, v, page_table, start, count, workspace, stream) */
@@ -302,6 +308,7 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t shape[4] = {-1, -1, 0, 0};
   size_t bytes;
   void* s;
+  int rc;
   (void)self;
   if (count_args(n, 8) || cache(&c, a[0], &kv)) return NULL;
   shape[2] = kv.H;
@@ -310,9 +317,12 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       table(&c, a[3], &tb, k.shape[0]) || lengths(&c, a[4], &first, "start", k.shape[0], 1) ||
       lengths(&c, a[5], &count, "count", k.shape[0], 1) || workspace(&c, a[6], &ws, &bytes) || stream_of(&c, a[7], &s))
     return NULL;
-  return done(&c, p_append(&kv, as_view(&k), as_view(&v), (const int32_t*)tb.ptr, (int)tb.shape[1],
-                           (const int32_t*)first.ptr, (const int32_t*)count.ptr, (int)k.shape[0], (int)k.shape[1],
-                           ws.ptr, bytes, s));
+  Py_BEGIN_ALLOW_THREADS
+  rc = p_append(&kv, as_view(&k), as_view(&v), (const int32_t*)tb.ptr, (int)tb.shape[1],
+                (const int32_t*)first.ptr, (const int32_t*)count.ptr, (int)k.shape[0], (int)k.shape[1],
+                ws.ptr, bytes, s);
+  Py_END_ALLOW_THREADS
+  return done(&c, rc);
 }
 
 /* read(cache, page_table, start, count, k_out, v_out, workspace, stream) */
@@ -324,6 +334,7 @@ static PyObject* read_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t shape[4] = {-1, -1, 0, 0};
   size_t bytes;
   void* s;
+  int rc;
   (void)self;
   if (count_args(n, 8) || cache(&c, a[0], &kv)) return NULL;
   shape[2] = kv.H;
@@ -340,9 +351,12 @@ static PyObject* read_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (table(&c, a[1], &tb, like->shape[0]) || lengths(&c, a[2], &first, "start", like->shape[0], 1) ||
       lengths(&c, a[3], &count, "count", like->shape[0], 1) || workspace(&c, a[6], &ws, &bytes) || stream_of(&c, a[7], &s))
     return NULL;
-  return done(&c, p_read(&kv, (const int32_t*)tb.ptr, (int)tb.shape[1], (const int32_t*)first.ptr,
-                         (const int32_t*)count.ptr, k.ptr, k.stride[0], k.stride[1], k.stride[2], v.ptr, v.stride[0],
-                         v.stride[1], v.stride[2], (int)like->shape[0], (int)like->shape[1], ws.ptr, bytes, s));
+  Py_BEGIN_ALLOW_THREADS
+  rc = p_read(&kv, (const int32_t*)tb.ptr, (int)tb.shape[1], (const int32_t*)first.ptr,
+              (const int32_t*)count.ptr, k.ptr, k.stride[0], k.stride[1], k.stride[2], v.ptr, v.stride[0],
+              v.stride[1], v.stride[2], (int)like->shape[0], (int)like->shape[1], ws.ptr, bytes, s);
+  Py_END_ALLOW_THREADS
+  return done(&c, rc);
 }
 
 /* attn(q, cache, page_table, context, count, mask, out, lse, sm_scale, workspace, stream) */
@@ -354,6 +368,7 @@ static PyObject* attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   double scale;
   size_t bytes;
   void* s;
+  int rc;
   (void)self;
   if (count_args(n, 11) || cache(&c, a[1], &kv)) return NULL;
   shape[3] = kv.D;
@@ -374,10 +389,13 @@ static PyObject* attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return NULL;
   scale = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred() || stream_of(&c, a[10], &s)) return NULL;
-  return done(&c, p_attn(as_view(&q), &kv, (const int32_t*)tb.ptr, (int)tb.shape[1], (const int32_t*)ctx.ptr,
-                         (const int32_t*)count.ptr, (const uint32_t*)mask.ptr, out.ptr, out.stride[0], out.stride[1],
-                         out.stride[2], (float*)lse.ptr, (int)q.shape[0], (int)q.shape[1], (int)q.shape[2],
-                         (float)scale, ws.ptr, bytes, s));
+  Py_BEGIN_ALLOW_THREADS
+  rc = p_attn(as_view(&q), &kv, (const int32_t*)tb.ptr, (int)tb.shape[1], (const int32_t*)ctx.ptr,
+              (const int32_t*)count.ptr, (const uint32_t*)mask.ptr, out.ptr, out.stride[0], out.stride[1],
+              out.stride[2], (float*)lse.ptr, (int)q.shape[0], (int)q.shape[1], (int)q.shape[2],
+              (float)scale, ws.ptr, bytes, s);
+  Py_END_ALLOW_THREADS
+  return done(&c, rc);
 }
 
 /* bind(rope, append, read, attn: function addresses; SageError) */

@@ -1,0 +1,93 @@
+"""The serving binding without a GPU: a child process in which torch's two device queries are replaced, tensors are objects
+with a tensor's attributes, and the library's functions are ones that report on their call; and its build."""
+import importlib.machinery
+import os
+import subprocess
+import sys
+import sysconfig
+import textwrap
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+CALLEE = """
+#include <unistd.h>
+static volatile int flag;
+void set_flag(int v) { flag = v; }
+int until_flag(void) {  /* at most three seconds */
+  for (int i = 0; i < 3000 && !flag; ++i) usleep(1000);
+  return flag ? 0 : 77;
+}
+int zero(void) { return 0; }
+"""
+
+CHILD = """
+import ctypes, importlib.machinery, importlib.util, sys, threading, time
+sys.path.insert(0, {root!r})
+import torch
+torch._C._cuda_getDevice = lambda: 0
+torch._C._cuda_getCurrentRawStream = lambda device: 0
+from fp8_quantized_exact_b200 import SageError, build
+loader = importlib.machinery.ExtensionFileLoader("_sage_serving", build.SERVING)
+m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_sage_serving", loader))
+loader.exec_module(m)
+callee = ctypes.CDLL({callee!r})
+address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+
+class Tensor:
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, shape
+    def stride(self):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.insert(0, s[0] * n)
+        return tuple(s)
+    def get_device(self): return 0
+    def data_ptr(self): return 4096
+    def element_size(self): return 1
+
+i32, bf16 = torch.int32, torch.bfloat16
+cache = (Tensor(torch.int8, 4, 2, 16, 64), Tensor(torch.float32, 4, 2, 16)) * 2
+x, q = Tensor(bf16, 3, 5, 2, 64), Tensor(bf16, 3, 5, 4, 64)
+table, lens, ws = Tensor(i32, 3, 2), Tensor(i32, 3), Tensor(torch.uint8, 1024)
+calls = dict(rope=[q, x, q, x, None, Tensor(torch.float64, 32), 1.0, 0, None, False, None],
+             append=[cache, x, x, table, lens, None, ws, None],
+             read=[cache, table, lens, None, x, x, ws, None],
+             attn=[q, cache, table, lens, None, None, q, None, 0.0, ws, None])
+{body}
+"""
+
+
+@pytest.fixture(scope="module")
+def build():
+    from fp8_quantized_exact_b200 import build as b
+    b.build()
+    return b
+
+
+def child(tmp_path, body):
+    src, so = tmp_path / "callee.c", tmp_path / "callee.so"
+    src.write_text(CALLEE)
+    subprocess.check_call([os.environ.get("CC", "gcc"), "-O1", "-fPIC", "-shared", str(src), "-o", str(so)])
+    code = CHILD.format(root=ROOT, callee=str(so), body=textwrap.dedent(body))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_calls_let_other_threads_run(build, tmp_path):
+    """A launch may block; what it waits for may be a Python thread's to do."""
+    child(tmp_path, """
+        m.bind(*[address(callee.until_flag)] * 4, SageError)
+        for name, args in calls.items():
+            callee.set_flag(0)
+            def free():
+                time.sleep(0.1)
+                callee.set_flag(1)
+            t = threading.Thread(target=free)
+            t.start()
+            getattr(m, name)(*args)  # SageError(77) where the other thread could not set the flag
+            t.join()
+    """)
