@@ -63,7 +63,11 @@ static int get(call* c, PyObject* o, tensor* t, const char* name) {
   PyObject* x;
   long dev;
   Py_ssize_t n;
-  if (!(x = PyObject_GetAttr(o, s_dtype))) return -1;
+  if (!(x = PyObject_GetAttr(o, s_dtype))) {
+    if (PyErr_ExceptionMatches(PyExc_AttributeError))
+      PyErr_Format(PyExc_ValueError, "%s: %s must be a tensor, not %s", c->what, name, Py_TYPE(o)->tp_name);
+    return -1;
+  }
   t->dtype = x;
   Py_DECREF(x);
   dev = as_long(PyObject_CallMethodNoArgs(o, s_get_device));
@@ -149,8 +153,12 @@ static int cache(call* c, PyObject* o, sage_cache* k) {
                             "float32 [pages, H, page_size]";
   tensor t[4];
   int i, f[2];
-  PyObject* seq = PySequence_Fast(o, "the cache must be a sequence (k, k_scale, v, v_scale)");
-  if (!seq) return -1;
+  PyObject* seq = PySequence_Fast(o, "");
+  if (!seq) {
+    if (!PyErr_ExceptionMatches(PyExc_TypeError)) return -1;
+    PyErr_Clear();
+    return bad(c, "the cache", must);
+  }
   if (PySequence_Fast_GET_SIZE(seq) != 4) {
     Py_DECREF(seq);
     return bad(c, "the cache", must);
@@ -256,13 +264,14 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t half[1] = {-1}, kshape[4];
   sage_view_bf16 vk = {NULL, 0, 0, 0};
   long layout, rot;
-  int inverse, has_pos = a[4] != Py_None, has_k;
+  int inverse, has_pos, has_k;
   double mscale;
   void* s;
   int rc;
   (void)self;
   if (count_args(n, 11)) return NULL;
   has_k = a[1] != Py_None;
+  has_pos = a[4] != Py_None;
   if (view(&c, a[0], &q, "q", any) || sizes(&c, &q) || view(&c, a[2], &qo, "q_out", q.shape)) return NULL;
   memset(&ko, 0, sizeof ko);
   memset(&k, 0, sizeof k);

@@ -91,3 +91,31 @@ def test_calls_let_other_threads_run(build, tmp_path):
             getattr(m, name)(*args)  # SageError(77) where the other thread could not set the flag
             t.join()
     """)
+
+
+def test_wrong_arguments(build, tmp_path):
+    """Too few or many arguments, None for a tensor that is not optional, and an object that is no tensor."""
+    child(tmp_path, """
+        m.bind(*[address(callee.zero)] * 4, SageError)
+        optional = dict(rope={1, 4, 8, 10}, append={4, 5, 7}, read={2, 3, 4, 5, 7}, attn={4, 5, 7, 10})
+        def refused(error, name, args):
+            try:
+                getattr(m, name)(*args)
+            except error:
+                return
+            raise AssertionError((name, error, len(args)))
+        for name, args in calls.items():
+            assert getattr(m, name)(*args) is None
+            for n in (0, 1, 2, 3, 4, len(args) - 1):
+                refused(TypeError, name, args[:n])
+            refused(TypeError, name, args + [None])
+            for i, a in enumerate(args):
+                if isinstance(a, Tensor):
+                    for other in (3, "x", [1]) + (() if i in optional[name] else (None,)):
+                        refused(ValueError, name, args[:i] + [other] + args[i + 1:])
+        refused(ValueError, "append", [None] + calls["append"][1:])
+        refused(ValueError, "append", [cache[:3] + (None,)] + calls["append"][1:])
+        refused(ValueError, "append", [cache[:3]] + calls["append"][1:])
+        refused(ValueError, "rope", calls["rope"][:3] + [None] + calls["rope"][4:])
+        refused(ValueError, "read", calls["read"][:4] + [None, None] + calls["read"][6:])
+    """)
