@@ -13,7 +13,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsage_b200.so")
-SERVING = os.path.join(BUILD, "_sage_serving.so")
+# with the ABI tag in its name, so that another Python version in the same tree builds and loads its own
+SERVING = os.path.join(BUILD, "_sage_serving" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [

@@ -22,6 +22,7 @@ import os
 import torch
 
 import fp8_quantized_exact_b200 as _sage
+from fp8_quantized_exact_b200 import build
 from fp8_quantized_exact_b200 import (SAGE_CACHE_E4M3, SAGE_CACHE_INT8, SAGE_ROPE_HALF, SAGE_ROPE_PLAIN, SageError,
                                       sage_rope_config)
 
@@ -36,7 +37,7 @@ def _calls():
     lib = _sage.lib()
     if _bound is not lib:
         if _native is None:
-            path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "_sage_serving.so")
+            path = build.SERVING
             if not os.path.exists(path):
                 raise RuntimeError(f"serving module not built: {path} is missing (run __graft_entry__.build())")
             loader = importlib.machinery.ExtensionFileLoader("_sage_serving", path)

@@ -119,3 +119,11 @@ def test_wrong_arguments(build, tmp_path):
         refused(ValueError, "rope", calls["rope"][:3] + [None] + calls["rope"][4:])
         refused(ValueError, "read", calls["read"][:4] + [None, None] + calls["read"][6:])
     """)
+
+
+def test_module_is_the_interpreters_own(build):
+    """Its name has the ABI tag, so that another Python version builds and loads one of its own."""
+    assert build.SERVING.endswith("_sage_serving" + sysconfig.get_config_var("EXT_SUFFIX"))
+    assert sysconfig.get_config_var("EXT_SUFFIX") in importlib.machinery.EXTENSION_SUFFIXES
+    from fp8_quantized_exact_b200 import serving
+    assert os.path.samefile(serving._calls().__spec__.origin, build.SERVING)
