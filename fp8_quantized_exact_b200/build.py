@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -36,7 +37,8 @@ def _stale(target, deps):
 
 
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
-    """Compile every .cu under csrc/ and link libsage_b200.so (static cudart)."""
+    """Compile every .cu under csrc/ and link libsage_b200.so (static cudart);
+    then the serving module."""
     os.makedirs(BUILD, exist_ok=True)
     headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
     objs = []
@@ -53,14 +55,25 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
                                "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    build_serving(force)
+    return LIB
+
+
+def build_serving(force: bool = False) -> None:
+    """Compile the CPython module of the serving calls.  Where the interpreter's
+    headers or a C compiler are missing it is left out, with a message: the
+    library and the other calls do not need it, and a serving call says so."""
     src = os.path.join(CSRC, "serving_py.c")
     if force or _stale(SERVING, [src, os.path.join(ROOT, "include", "sage_b200.h")]):
+        cc, include = os.environ.get("CC", "gcc"), sysconfig.get_paths()["include"]
+        if not os.path.exists(os.path.join(include, "Python.h")) or not shutil.which(cc.split()[0]):
+            print(f"serving module not built: it needs {os.path.join(include, 'Python.h')} and {cc}", file=sys.stderr)
+            return
         tmp = SERVING + f".tmp{os.getpid()}"
-        subprocess.check_call([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared",
-                               "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"), "-I",
-                               sysconfig.get_paths()["include"], src, "-o", tmp])
+        subprocess.check_call(cc.split() + ["-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared",
+                               "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"), "-I", include, src, "-o",
+                               tmp])
         os.replace(tmp, SERVING)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -127,3 +127,19 @@ def test_module_is_the_interpreters_own(build):
     assert sysconfig.get_config_var("EXT_SUFFIX") in importlib.machinery.EXTENSION_SUFFIXES
     from fp8_quantized_exact_b200 import serving
     assert os.path.samefile(serving._calls().__spec__.origin, build.SERVING)
+
+
+def test_library_builds_without_python_headers(build, tmp_path, monkeypatch, capsys):
+    """The library needs nvcc alone; the serving calls then say what is missing."""
+    import fp8_quantized_exact_b200 as sage
+    from fp8_quantized_exact_b200 import serving
+    missing = str(tmp_path / "_sage_serving.so")
+    monkeypatch.setattr(build, "SERVING", missing)
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert build.build() == build.LIB
+    assert not os.path.exists(missing) and "Python.h" in capsys.readouterr().err
+    monkeypatch.setattr(serving, "_native", None)
+    monkeypatch.setattr(serving, "_bound", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        sage.sage_rope(None, None, None, None, None, None)
+    assert sage.sage_workspace_bytes(sage.SAGE_OP_CACHE, 1, 1, 1, 64) > 0
