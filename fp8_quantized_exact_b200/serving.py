@@ -23,8 +23,8 @@ import torch
 
 import fp8_quantized_exact_b200 as _sage
 from fp8_quantized_exact_b200 import build
-from fp8_quantized_exact_b200 import (SAGE_CACHE_E4M3, SAGE_CACHE_INT8, SAGE_ROPE_HALF, SAGE_ROPE_PLAIN, SageError,
-                                      sage_rope_config)
+from fp8_quantized_exact_b200 import (SAGE_CACHE_E4M3, SAGE_CACHE_INT8, SAGE_ROPE_HALF, SAGE_ROPE_PLAIN,
+                                      SAGE_STATUS_BYTES, SageError, sage_rope_config)
 
 _FORMAT = {torch.int8: SAGE_CACHE_INT8, torch.float8_e4m3fn: SAGE_CACHE_E4M3}
 _bound = None
@@ -101,6 +101,10 @@ def sage_cache_attn(q, cache, page_table, context, count, mask, out, lse, sm_sca
 
 def sage_clear_device_status(workspace, stream=None):
     """Zero the workspace's status block."""
+    if (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous() or
+            workspace.numel() * workspace.element_size() < SAGE_STATUS_BYTES):
+        raise ValueError("sage_clear_device_status: workspace must be a contiguous CUDA tensor of at least "
+                         f"{SAGE_STATUS_BYTES} bytes")
     _check(_sage.lib().sage_clear_device_status(workspace.data_ptr(), _sage._stream(stream)), "sage_clear_device_status")
 
 

@@ -143,3 +143,10 @@ def test_library_builds_without_python_headers(build, tmp_path, monkeypatch, cap
     with pytest.raises(RuntimeError, match="not built"):
         sage.sage_rope(None, None, None, None, None, None)
     assert sage.sage_workspace_bytes(sage.SAGE_OP_CACHE, 1, 1, 1, 64) > 0
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1024, dtype=torch.uint8), None])
+def test_clear_status_refuses_what_is_no_device_workspace(build, workspace):
+    import fp8_quantized_exact_b200 as sage
+    with pytest.raises(ValueError):
+        sage.sage_clear_device_status(workspace)
