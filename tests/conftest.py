@@ -16,3 +16,18 @@ def pytest_configure(config):
 @pytest.fixture(scope="session")
 def golden_dir():
     return os.path.join(ROOT, "tests", "golden")
+
+
+@pytest.fixture(autouse=True)
+def structures_outlive_their_addresses(request, monkeypatch):
+    """Keeps what a module's cache_struct() makes until its test ends: ctypes.addressof(cache_struct()) alone holds no
+    reference, and the library would read memory that may have been given out again."""
+    make = getattr(request.module, "cache_struct", None)
+    if make is not None:
+        kept = []
+
+        def cache_struct(**kw):
+            kept.append(make(**kw))
+            return kept[-1]
+        monkeypatch.setattr(request.module, "cache_struct", cache_struct)
+    yield
