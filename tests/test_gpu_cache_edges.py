@@ -96,3 +96,42 @@ def test_append_ties_of_the_largest_values(sage, fmt, power):
     code, scale = cu.quantise(x[0, :, 0], dt)
     assert torch.equal(cache[0].double().permute(0, 2, 1, 3).reshape(-1, D)[:n], code)
     assert torch.equal(cache[1].permute(0, 2, 1).reshape(-1)[:n], scale)
+
+
+@pytest.mark.parametrize("B,T,G,H,D", [(1, 1, 4, 8, 128), (3, 21, 4, 2, 64)])
+def test_calls_behind_an_eager_fork_of_streams(sage, B, T, G, H, D):
+    """A loop whose append runs on a second stream, forked from and joined to the first by events, while the first stream
+    rotates Q: the bits of the same loop on an idle device."""
+    n, steps = 1500, 16
+    results = []
+    for idle in (True, False):
+        cache, table, ws, q = problem(sage, B, T, G, H, D, n + steps * T, seed=3)
+        ws2 = sage.workspace(sage.SAGE_OP_CACHE, 1, 1, 1, D)
+        f, m = sage.sage_rope_freqs(D)
+        ctx = torch.full((B,), n, dtype=torch.int32, device=DEV)
+        out, k = torch.empty_like(q), torch.empty(B, T, H, D, dtype=torch.bfloat16, device=DEV)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        wait = torch.cuda.synchronize if idle else (lambda: None)
+        for _ in range(steps):
+            k.copy_(q[:, :, ::G])
+            wait()
+            side.wait_stream(torch.cuda.current_stream())
+            sage.sage_cache_append(cache, k, k, table, ctx, None, ws2, stream=side)
+            wait()
+            sage.sage_rope(q, None, q, None, None, f, m)
+            wait()
+            torch.cuda.current_stream().wait_stream(side)
+            sage.sage_cache_attn(q, cache, table, ctx, None, None, out, None, 0.0, ws)
+            wait()
+            q.copy_(out).mul_(8.0)
+            ctx.add_(T)
+            wait()
+        torch.cuda.synchronize()
+        assert sage.sage_read_device_status(ws) == sage.sage_read_device_status(ws2) == sage.SAGE_OK
+        back = torch.empty(B, n + steps * T, H, D, dtype=torch.bfloat16, device=DEV)  # the slots that were written
+        sage.sage_cache_read(cache, table, None, None, back, None, ws)
+        results.append((q, back))
+    assert all(torch.isfinite(t).all() for t in results[0])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
