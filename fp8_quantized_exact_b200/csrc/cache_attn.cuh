@@ -81,11 +81,11 @@ __device__ __forceinline__ Stretch find_stretch(const CacheAttnArgs& a, int cta,
   t.own.n = t.own.rt = 1;
   t.own.per = 0;
   if (lane < a.B) t.own = seq_of<TILE, R>(a, lane);
-  unsigned sum = t.own.per, longest = t.own.n;
+  unsigned sum = t.own.per, longest = t.own.per ? t.own.n : 0;  // a sequence without rows has no unit
   for (int b = lane + 32; b < a.B; b += 32) {
     const Seq s = seq_of<TILE, R>(a, b);
     sum += s.per;
-    longest = max(longest, s.n);
+    if (s.per) longest = max(longest, s.n);
   }
   t.total = __reduce_add_sync(0xffffffffu, sum);
   t.share = max((t.total + ctas * STEP - 1) / (ctas * STEP), 1u) * STEP;

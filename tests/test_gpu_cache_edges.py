@@ -135,3 +135,26 @@ def test_calls_behind_an_eager_fork_of_streams(sage, B, T, G, H, D):
     assert all(torch.isfinite(t).all() for t in results[0])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_a_sequence_without_rows_does_not_slow_the_others(sage):
+    """A long context that has no drafted token in this call takes no part in how the others are cut."""
+    B, T, G, D, n = 9, 64, 2, 128, 4096
+    cache, table, ws, q = problem(sage, B, T, G, 1, D, 150000 // 32, seed=5)
+    table = torch.cat((table, torch.full((B, 150000 // 64), -1, dtype=torch.int32, device=DEV)), 1).contiguous()
+    count = torch.tensor([0] + [T] * (B - 1), dtype=torch.int32, device=DEV)
+    out = torch.empty_like(q)
+    times = {}
+    for first in (0, 150000, 0, 150000):
+        ctx = torch.tensor([first] + [n] * (B - 1), dtype=torch.int32, device=DEV)
+        for _ in range(3):
+            sage.sage_cache_attn(q, cache, table, ctx, count, None, out, None, 0.0, ws)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(50):
+            sage.sage_cache_attn(q, cache, table, ctx, count, None, out, None, 0.0, ws)
+        b.record()
+        torch.cuda.synchronize()
+        times[first] = min(times.get(first, 1e9), a.elapsed_time(b) / 50)
+    assert sage.sage_read_device_status(ws) == sage.SAGE_OK
+    assert times[150000] <= 1.5 * times[0], times
