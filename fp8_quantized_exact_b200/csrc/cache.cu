@@ -23,7 +23,7 @@
 // a row, so that its lookups and scale cost little per element, and eight
 // neighbouring tokens of a head lie in one warp: their scales are one 32-byte
 // sector and their codes are contiguous in the page.  Measured on B200: append of
-// 16 prompts of 37..8192 tokens, 8 heads of 128, 80 us (68 at the copy rate; with a thread per row and a
+// 16 prompts of 37..8192 tokens, 8 heads of 128, 80 to 90 us by the box (68 at the copy rate; with a thread per row and a
 // division per element 168); read of 4 contexts of 1000..37810, 107 us (102; 162 with a thread per row).
 #include "cache_codes.cuh"
 #include "cache_common.cuh"

@@ -607,7 +607,7 @@ size_t cache_attn_workspace_bytes() { return kPartBytes + kCutBytes; }
 int launch_cache_attn(const CacheAttnArgs& a, cudaStream_t s) {
   // The tcgen05 variant takes 128 rows at once at nearly the time of 16; this one reads and converts the cache again for
   // each 16.  Measured on B200 (us here against there, cold L2, 16 sequences of 500..16384, 8 heads): D = 128: 16 rows
-  // 100 / 170, 32 rows 166 / 173, 40 rows 219 / 174; D = 64: 32 rows 100 / 145, 48 rows 129 / 145, 56 rows 156 / 148.
+  // 101 / 167, 32 rows 169 / 169, 40 rows 220 / 169; D = 64: 32 rows 105 / 154, 48 rows 132 / 157, 56 rows 161 / 157.
   if (a.T * a.G > (a.c.D == 128 ? 32 : 48)) return launch_cache_attn_tc(a, s);
   return a.c.D == 128 ? by_rows<128>(a, s) : by_rows<64>(a, s);
 }

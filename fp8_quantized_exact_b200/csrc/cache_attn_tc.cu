@@ -21,10 +21,13 @@
 //                    tile touches) and of their scales (bulk copies).
 //   warps 18, 19     QK and PV issuers; the A operands, Q and P, are in TMEM.
 // What bounds it: the instructions and waits of the roles, not a pipe.  A tile of 64
-// keys takes about 1,900 cycles on an SM at 128 rows (tensor pipe 26% busy, issue
-// slots 46%) and little less at 16 rows; an M = 128 MMA costs its issuer about 65
-// cycles for any N up to 128.  Tried and not kept, as factors of the time of 64 drafted
-// tokens over 4 contexts of 20000..37810 (424 us then, 409 now): pairs of tiles per QK MMA 1.27, P in
+// keys takes 1,600 (64 drafted tokens over 4 contexts of 20000..37810: tensor pipe 32% busy,
+// issue slots 62%) to 1,900 cycles (21 over 16 of 500..16384: 27%, 53%) on an SM, with about 1,000
+// instructions per scheduler, and little less at 16 rows; an M = 128 MMA costs its issuer about 65
+// cycles for any N up to 128.  272 bytes of registers are spilled (96 a thread), mostly by the masked form.
+// Four roles share the way of instructions to the SM, so their layout counts: see set_offsets and
+// MaskedRows.  Tried and not kept, as factors of the time of 64 drafted
+// tokens over 4 contexts of 20000..37810 (424 us then, 449 to 469 by the box now): pairs of tiles per QK MMA 1.27, P in
 // columns of its own with Q in shared memory 1.05, one QK issuer per stream 1.25,
 // both score loads of a half before one wait 1.12, two converter warps per side
 // instead of four 1.22, 32x32b loads with every scale read by every thread 1.15.

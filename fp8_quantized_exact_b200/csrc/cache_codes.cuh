@@ -103,7 +103,8 @@ __device__ __forceinline__ float q_factor(int eq) { return __int_as_float((127 +
 // 11 bits; the others are off by at most 2^-32 of the largest.  p itself is FP32 and may be large.
 constexpr float kHead = 8.0f;   // when c is set, the tile's largest weight is in (2^(kHead - 1), 2^kHead]
 constexpr float kLimit = 15.0f;  // scores that pass c by more raise it (log2)
-constexpr float kLow = 88.0f;    // p stays at or below 2^(kLow + kHead), however small the weights beside it are
+constexpr float kLow = 88.0f;    // p stays at or below 2^(kLow + kHead), however small the weights beside it are (an lse of such a
+                                 // row is off by up to 2^-18, FP32's step of its s - c)
 constexpr float kMass = 100.0f;  // a row's sum stays below 2^kMass when c is lowered because E grew
 
 // c for a tile whose largest score is `top` and whose largest score plus log2 of its V scale is `weight` (rounded up): an

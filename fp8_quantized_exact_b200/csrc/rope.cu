@@ -97,7 +97,7 @@ struct TokenRows {
 // B*N of the batch, the heads Q's Hq then K's.  A thread takes one item of
 // ROWS rows at a time, their loads issued together: one row in the half layout,
 // whose items have two loads already, four in the interleaved one (measured on
-// B200 with 1, 2 and 4 rows: 343, 379, 399 us for the half layout at B1 N37810
+// B200 with 1, 2 and 4 rows: 343 (337 to 371 by the box), 379, 399 us for the half layout at B1 N37810
 // 56+56 heads D128, 331 us at the copy rate; 141, 138, 135 us for the interleaved
 // one at B4 N16384 24+24 heads D64 rot 32, 123 us at the copy rate).
 template <bool HALF, bool VEC>
