@@ -15,7 +15,7 @@
 //
 // Online softmax per row in base 2: FP32 sums l += p_j and O += w_j code_j,
 // p_j = 2^(s_j - c) and w_j = p_j vscale_j 2^-E rounded to FP16 (2^-11), for which
-// c keeps the row's largest weight near 2^10 (cache_codes.cuh says why).  c is set
+// c keeps the row's largest weight near 2^8 (cache_codes.cuh says why).  c is set
 // again only when a score passes it by more than 15 or a V scale passes 2^E, which
 // one vote per tile finds out: later tiles need no reduction across lanes.  E is an
 // integer per row with 2^E at or above the largest V scale that the row has seen; it

@@ -429,7 +429,8 @@ enum sage_cache_format {
 
 typedef struct sage_cache {
   void* k_codes;  /* [pages][H][page_size][D], one byte each */
-  float* k_scale; /* [pages][H][page_size] */
+  float* k_scale; /* [pages][H][page_size]; not negative (NaN: a row that spoils
+                     what sees it) */
   void* v_codes;
   float* v_scale;
   int k_format, v_format; /* enum sage_cache_format */

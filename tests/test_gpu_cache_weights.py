@@ -53,10 +53,15 @@ def problem(sage, n, T, G, D, vf, score, vscale, seed):
     return q, cache, torch.arange(pages, dtype=torch.int32, device=DEV)[None], kc, ks, vc, vs
 
 
-def check(sage, n, T, G, D, vf, score, vscale, B, seed):
+def check(sage, n, T, G, D, vf, score, vscale, B, seed, left_out=()):
     """B sequences share the pages, so that there are enough units (sequence and head) for each to lie in one stretch of
-    the work list, or few enough that each is cut; all give the same rows but for where they are cut."""
+    the work list, or few enough that each is cut; all give the same rows but for where they are cut.  left_out: pages
+    whose table entry names none."""
     q, cache, table, kc, ks, vc, vs = problem(sage, n, T, G, D, vf, score, vscale, seed)
+    keep = torch.ones(n, dtype=torch.bool)
+    for page in left_out:
+        table[0, page] = -1
+        keep[page * PAGE:(page + 1) * PAGE] = False
     H = ks.shape[0]
     ws = sage.workspace(sage.SAGE_OP_CACHE_ATTN, 1, 1, 1, D)
     out = torch.full((B, T, H * G, D), 5.0, dtype=torch.bfloat16, device=DEV)
@@ -64,11 +69,12 @@ def check(sage, n, T, G, D, vf, score, vscale, B, seed):
     sage.sage_cache_attn(q.expand(B, -1, -1, -1), cache, table.expand(B, -1).contiguous(),
                          torch.full((B,), n, dtype=torch.int32, device=DEV), None, None, out, lse, 0.0, ws)
     torch.cuda.synchronize()
-    assert sage.sage_read_device_status(ws) == sage.SAGE_OK
-    kk = kc[:, :n].double().to(DEV) * ks[:, :n, None].double().to(DEV)
+    assert sage.sage_read_device_status(ws) == (sage.SAGE_ERR_DEVICE if left_out else sage.SAGE_OK)
+    kc, ks, vc, vs = (x[:, :n][:, keep] for x in (kc, ks, vc, vs))
+    kk = kc.double().to(DEV) * ks[..., None].double().to(DEV)
     s = (kk @ q[0, 0, 0].double()) * D ** -0.5  # [H, n]; the drafted tokens' share is below e^-30 of the smallest
     p = torch.softmax(s, -1)
-    v = vc[:, :n].double().to(DEV) * vs[:, :n, None].double().to(DEV)
+    v = vc.double().to(DEV) * vs[..., None].double().to(DEV)
     want = torch.einsum("hn,hnd->hd", p, v)
     spread = torch.einsum("hn,hnd->hd", p, v.abs())
     # a score is an FP32 sum of D products of one sign and three more roundings: (D + 4) 2^-24 of itself, which moves p and
@@ -163,6 +169,18 @@ def test_scores_that_do_not_differ_and_that_climb(sage, kind, T, G, D):
     if kind == "steps":
         s = s + torch.arange(n, dtype=torch.float64) // 32 * 0.7
     check(sage, n, T, G, D, E4M3, s, torch.ones(H, n, dtype=torch.float64), count(T, G, D, WHOLE), seed=2)
+
+
+@pytest.mark.parametrize("T,G,D", SHAPES)
+@pytest.mark.parametrize("B", [WHOLE, CUT])
+@pytest.mark.parametrize("kind", ["rising", "wild"])
+def test_pages_left_out_between_value_scales(sage, kind, B, T, G, D):
+    """Pages left out in the middle of a context (tiles that not every group of keys has), with V scales that grow before,
+    on and behind them."""
+    H, n = 8, 4000
+    s = noise(H, n, 2.0, 9)
+    vs = torch.exp(4.0 * noise(H, n, 1.0, 10)) if kind == "wild" else torch.exp2(torch.linspace(-20.0, 20.0, n, dtype=torch.float64)).expand(H, n)
+    check(sage, n, T, G, D, INT8 if D == 64 else E4M3, s, vs, count(T, G, D, B), seed=3, left_out=(0, 7, 8, 19, 30))
 
 
 @pytest.mark.parametrize("T,G,D", SHAPES)
