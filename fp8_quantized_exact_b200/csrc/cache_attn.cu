@@ -502,7 +502,7 @@ __global__ void __maxnreg__((Shape<D, NT>::kRegs))
       for (int e = 0; e < 2; ++e) {
         const int lr = 8 * nt + 2 * c4 + e;
         const float up = __int_as_float((254 << 23) - __float_as_int(e ? dn.y : dn.x));  // 2^E
-        const Mass m = normalised(rs[nt].thr[e] == -INFINITY ? -INFINITY : -(e ? nc.y : nc.x), e ? l2.y : l2.x);
+        const Mass m = normalised(rs[nt].thr[e] == -INFINITY ? -INFINITY : -(e ? nc.y : nc.x), e ? l2.y : l2.x, kPartBias);
         if (lr >= rows) continue;
         if (whole) {
           const OutRow to(a, b, h, row0 + lr);

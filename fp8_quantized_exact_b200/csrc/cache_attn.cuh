@@ -201,7 +201,7 @@ __device__ __forceinline__ float row_inverse(float l) { return l == 0.0f ? 0.0f 
 __device__ __forceinline__ void store_lse(const CacheAttnArgs& a, int b, int h, int row, float c, float l) {
   if (!a.lse) return;
   const int t = row / a.G, hq = h * a.G + row % a.G;
-  const Mass m = normalised(c, l);
+  const Mass m = normalised(c, l, 0);
   a.lse[((int64_t)b * a.T + t) * a.Hq + hq] = l == 0.0f ? -INFINITY : (m.c + log2f(m.l)) * 0.693147180559945f;
 }
 

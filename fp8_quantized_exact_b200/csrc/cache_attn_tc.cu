@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         if (c4 == 0) {
           const int rw = wrow + g + 8 * r;
-          const Mass m = normalised((st_rows.none >> r) & 1 ? -INFINITY : st_rows.c[r], x);
+          const Mass m = normalised((st_rows.none >> r) & 1 ? -INFINITY : st_rows.c[r], x, kPartBias);
           sm.l[sid][rw] = m.l;
           sm.c[sid][rw] = m.c;
           sm.g[sid][rw] = m.g;
@@ -613,11 +613,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const float ca = sm.c[0][row], cb = sm.c[1][row], cm = fmaxf(ca, cb);
         const float wa = ca == -INFINITY ? 0.0f : ex2(ca - cm), wb = cb == -INFINITY ? 0.0f : ex2(cb - cm);
         const float lt = sm.l[0][row] * wa + sm.l[1][row] * wb;
-        const float ga = sm.g[0][row], gb = sm.g[1][row];
         const bool has_a = sm.up[0][row] != 0.0f, has_b = sm.up[1][row] != 0.0f;
         const bool whole = seg == u.start && seg_end == unit_end, on = row < rows;
         const float inv = whole ? row_inverse(lt) : 1.0f;
-        const float fa = wa * sm.up[0][row] * inv, fb = wb * sm.up[1][row] * inv;
+        const float fa = sm.g[0][row] * wa * inv, fb = sm.g[1][row] * wb * inv, up_a = sm.up[0][row], up_b = sm.up[1][row];
         const OutRow out(a, b, h, min(row0 + row, cnt * a.G - 1));
         float* part = part_of<kRowsT, D>(a, blockIdx.x, seg == u.start ? 1 : 0);
 #pragma unroll 1
@@ -631,7 +630,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           float o[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            o[e] = (has_a ? __uint_as_float(oa[e]) * ga * fa : 0.0f) + (has_b ? __uint_as_float(ob[e]) * gb * fb : 0.0f);
+            o[e] = (has_a ? __uint_as_float(oa[e]) * fa * up_a : 0.0f) + (has_b ? __uint_as_float(ob[e]) * fb * up_b : 0.0f);
           if (on && whole) {
 #pragma unroll
             for (int e = 0; e < 16; e += 8)

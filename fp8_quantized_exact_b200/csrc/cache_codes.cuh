@@ -103,7 +103,7 @@ __device__ __forceinline__ float q_factor(int eq) { return __int_as_float((127 +
 // 11 bits; the others are off by at most 2^-32 of the largest.  p itself is FP32 and may be large.
 constexpr float kHead = 8.0f;   // when c is set, the tile's largest weight is in (2^(kHead - 1), 2^kHead]
 constexpr float kLimit = 15.0f;  // scores that pass c by more raise it (log2)
-constexpr float kLow = 88.0f;    // p stays at or below 2^(kLow + kHead), however small the weights beside it are (an lse of such a
+constexpr float kLow = 76.0f;    // p stays at or below 2^(kLow + kHead), however small the weights beside it are (an lse of such a
                                  // row is off by up to 2^-18, FP32's step of its s - c)
 constexpr float kMass = 100.0f;  // a row's sum stays below 2^kMass when c is lowered because E grew
 
@@ -119,12 +119,16 @@ __device__ __forceinline__ float kept_offset(float c, int de, float mass) {
   return __fadd_ru(c, -fminf((float)de, room));
 }
 
-// A row's sum l with its offset c as c' and l' in [1, 2), and g = l' / l: where l may be large, 2^E l is not.
+// A row's sum l with its offset c as c' and l' in [2^-bias, 2^(1-bias)), and g = l' / l: l may be large, and the row's
+// weighted sum is l times a mean of values.  What is joined has a bias: up to 12 parts of a CTA and then up to 148 of a
+// unit stay below the largest value in all (12 * 148 * 2^(1 - kPartBias) < 1).  l is below 2^113 by the limits above (2^28
+// keys), so g is a normal number.
 struct Mass {
   float c, l, g;
 };
-__device__ __forceinline__ Mass normalised(float c, float l) {
-  const int k = l > 0.0f && l < 0x1p127f ? (__float_as_int(l) >> 23) - 127 : 0;  // zero, infinity and NaN stay
+constexpr int kPartBias = 12;
+__device__ __forceinline__ Mass normalised(float c, float l, int bias) {
+  const int k = l > 0.0f && l < 0x1p127f ? (__float_as_int(l) >> 23) - 127 + bias : 0;  // zero, infinity and NaN stay
   if (k == 0) return {c, l, 1.0f};
   const float c2 = c + (float)k;  // rounded where c passes 2^24: the factor is of what it became
   float g;

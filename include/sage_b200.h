@@ -524,7 +524,7 @@ SAGE_API int sage_cache_read(const sage_cache* cache, const int32_t* page_table,
  *     of FP16 values, exact for the codes, with FP32 sums.  A weight, the
  *     probability times the V scale, is rounded to FP16: to 11 bits down to
  *     2^-21 of the row's largest weight, and off by at most 2^-32 of the largest
- *     below that, wherever the largest weight is at least 2^-88 of the product
+ *     below that, wherever the largest weight is at least 2^-76 of the product
  *     of the row's largest probability and largest V scale.
  *     Scores may have any size that FP32 holds, for K below 2^96 in magnitude.
  *   - lse (NULL or [B][T][Hq]): ln sum_j exp(s_j).

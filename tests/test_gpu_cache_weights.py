@@ -138,10 +138,11 @@ def test_key_of_huge_value_and_no_probability(sage, power, n, B, T, G, D):
 
 @pytest.mark.parametrize("T,G,D", SHAPES)
 @pytest.mark.parametrize("B", [WHOLE, CUT])
-@pytest.mark.parametrize("kind", ["rising", "falling", "wild", "against", "tiny", "large"])
+@pytest.mark.parametrize("kind", ["rising", "falling", "wild", "against", "tiny", "large", "largest"])
 def test_value_scales_over_many_orders(sage, kind, B, T, G, D):
     """V scales that rise or fall by 2^60 along the context with scores that undo most of it, that are wild, that are the
-    inverse of the probability (every key gives the same share), and that are all tiny or large."""
+    inverse of the probability (every key gives the same share), that are all tiny or large, and that put V at the largest
+    BF16 values."""
     H, n = 8, 4096
     s = noise(H, n, 2.0, 5)
     vs = torch.exp(0.3 * noise(H, n, 1.0, 6))
@@ -155,6 +156,8 @@ def test_value_scales_over_many_orders(sage, kind, B, T, G, D):
     elif kind == "against":
         s = noise(H, n, 8.0, 8)
         vs = torch.exp(-s)
+    elif kind == "largest":
+        vs = torch.full((H, n), 3.38e38 / (127 if D == 64 else 448), dtype=torch.float64)
     else:
         vs = vs * (1e-34 if kind == "tiny" else 1e30)
     check(sage, n, T, G, D, INT8 if D == 64 else E4M3, s, vs, count(T, G, D, B), seed=1)
